@@ -29,6 +29,9 @@ PATHS = {"auto": MOE_PATH_AUTO, "gemv": MOE_PATH_GEMV, "mfma": MOE_PATH_MFMA,
 EXPORTS = ("moe_workspace_bytes", "moe_forward", "moe_forward_static", "moe_forward_streamed", "moe_route",
            "moe_permute",
            "moe_dequant_e4m3", "moe_quantize_act_e4m3", "moe_workspace_region",
+           "moe_select_experts", "moe_route_gated", "moe_forward_gated",
+           "moe_linear_workspace_bytes", "moe_linear", "moe_linear_e4m3",
+           "moe_swiglu_quantize_e4m3",
            "moe_status_string", "moe_version", "moe_set_wait_limit")
 (MOE_WS_TOPK, MOE_WS_GATES, MOE_WS_OFFSETS, MOE_WS_PAIR, MOE_WS_INV, MOE_WS_H, MOE_WS_H_EXPS,
  MOE_WS_Y, MOE_WS_Y_EXPS, MOE_WS_STATUS, MOE_WS_COUNT) = range(11)
@@ -46,6 +49,21 @@ class MoeConfig(ctypes.Structure):
         ("x_dtype", ctypes.c_int),
         ("out_dtype", ctypes.c_int),
         ("path", ctypes.c_int),
+    ]
+
+
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = range(2)
+SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+
+
+class MoeGating(ctypes.Structure):
+    _fields_ = [
+        ("score", ctypes.c_int),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_rank", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -115,6 +133,19 @@ def load() -> ctypes.CDLL:
     lib.moe_dequant_e4m3.restype = ctypes.c_int
     lib.moe_quantize_act_e4m3.argtypes = [P, ctypes.c_int64, ctypes.c_int32, P, P, P]
     lib.moe_quantize_act_e4m3.restype = ctypes.c_int
+    gatep, I32, I64, SZ = ctypes.POINTER(MoeGating), ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    lib.moe_select_experts.argtypes = [P, ctypes.c_int, I64, P, gatep, I64, I32, I32, P, P, P]
+    lib.moe_route_gated.argtypes = [P, P, P, P, gatep, P, P, P, cfgp, P, SZ, P]
+    lib.moe_forward_gated.argtypes = [P, P, P, P, gatep, bankp, bankp, I32, P, cfgp, P, SZ,
+                                      ctypes.POINTER(MoePhaseEvents), P]
+    lib.moe_linear_workspace_bytes.argtypes = [I64, I32, I32, I32]
+    lib.moe_linear_workspace_bytes.restype = SZ
+    lib.moe_linear.argtypes = [P, I64, P, P, P, I64, I32, I32, P, I64, ctypes.c_int, P, SZ, P]
+    lib.moe_linear_e4m3.argtypes = [P, P, P, P, P, I64, I32, I32, P, I64, ctypes.c_int, P, SZ, P]
+    lib.moe_swiglu_quantize_e4m3.argtypes = [P, I64, I64, I32, P, P, P]
+    for name in ("moe_select_experts", "moe_route_gated", "moe_forward_gated", "moe_linear",
+                 "moe_linear_e4m3", "moe_swiglu_quantize_e4m3"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.moe_workspace_region.argtypes = [cfgp, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
                                          ctypes.POINTER(ctypes.c_size_t)]
     lib.moe_workspace_region.restype = ctypes.c_int
@@ -442,3 +473,225 @@ def moe_dequant_e4m3(w: torch.Tensor, scales: torch.Tensor, block: int,
     if st != MOE_OK:
         raise MoeError(st, "moe_dequant_e4m3")
     return out
+
+
+# ---- choice of experts by scores, and the dense block-FP8 operators ----
+# These take tensors of one device, which need not be the current one; with
+# `stream`, what they allocate belongs to that stream.
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_UNREAD = 256  # address given for an empty tensor, whose memory no call touches
+
+
+def _place(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> torch.device:
+    dev = first.device
+    for t in (first, *rest):
+        if t is not None and (t.device != dev or not t.is_cuda):
+            raise ValueError("tensors must be on one GPU")
+    return dev
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    """Distance in elements between the rows of a 2-D tensor with unit column
+    stride (columns broadcast or out of order are refused)."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{what} must be 2-D with contiguous rows")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    return t.stride(0)
+
+
+def _flat(t: Optional[torch.Tensor], shape, dtype, what: str):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)
+                          or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else (t.data_ptr() or _UNREAD)
+
+
+def _empty(shape, dtype, dev, stream):
+    if stream is None:
+        if dev.index == torch.cuda.current_device():
+            return torch.empty(shape, dtype=dtype, device=dev)
+        stream = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _enqueue(name: str, dev: torch.device, stream, *args):
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    fn = getattr(load(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    if st != MOE_OK:
+        raise MoeError(st, name)
+
+
+class Gating:
+    """How moe_select_experts, moe_route_gated and moe_forward_gated choose
+    experts (moe_gating): the score ("softmax" or "sigmoid"), the number of
+    expert groups, how many are kept, how many of a group's best experts make
+    its score (1 or 2), whether the gates are renormalised over the chosen
+    experts, and their factor."""
+    __slots__ = ("c", "ref")
+
+    def __init__(self, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+                 group_rank: int = 1, renormalise: bool = True, scale: float = 1.0):
+        if score not in SCORES:
+            raise ValueError(f"score must be one of {sorted(SCORES)}")
+        self.c = MoeGating(SCORES[score], groups, top_groups, group_rank, bool(renormalise), scale)
+        self.ref = ctypes.byref(self.c)
+
+
+def moe_select_experts(logits: torch.Tensor, top_k: int, gating: Gating,
+                       balance_bias: Optional[torch.Tensor] = None, stream=None):
+    """The gated choice of experts from logits [T][E] (fp32 or bf16):
+    (topk_idx [T][k] int32, gates [T][k] fp32)."""
+    dev = _place(logits, balance_bias)
+    ld = _rows(logits, "logits")
+    T, E = logits.shape
+    if logits.dtype not in _DTYPES:
+        raise ValueError("logits must be float32 or bfloat16")
+    _flat(balance_bias, (E,), torch.float32, "balance_bias")
+    idx = _empty((T, max(top_k, 0)), torch.int32, dev, stream)
+    gates = _empty((T, max(top_k, 0)), torch.float32, dev, stream)
+    _enqueue("moe_select_experts", dev, stream, _addr(logits), _DTYPES[logits.dtype], ld,
+             _addr(balance_bias), gating.ref, T, E, top_k, _addr(idx), _addr(gates))
+    return idx, gates
+
+
+def moe_route_gated(x: torch.Tensor, router_w: torch.Tensor, top_k: int, gating: Gating,
+                    inter: int, block: int, router_bias: Optional[torch.Tensor] = None,
+                    balance_bias: Optional[torch.Tensor] = None, with_logits: bool = False,
+                    workspace: Optional[torch.Tensor] = None, stream=None):
+    """Router and gated choice through moe_route_gated: (topk_idx, gates[, logits])."""
+    dev = _place(x, router_w, router_bias, balance_bias, workspace)
+    _dev(x)
+    T, H = x.shape
+    E = router_w.shape[0]
+    _flat(router_w, (E, H), torch.float32, "router_w")
+    _flat(router_bias, (E,), torch.float32, "router_bias")
+    _flat(balance_bias, (E,), torch.float32, "balance_bias")
+    cfg = make_config(T, H, E, inter, top_k, block, False, x.dtype, torch.float32)
+    idx = _empty((T, max(top_k, 0)), torch.int32, dev, stream)
+    gates = _empty((T, max(top_k, 0)), torch.float32, dev, stream)
+    logits = _empty((T, E), torch.float32, dev, stream) if with_logits else None
+    if workspace is None:
+        workspace = _empty(max(1, workspace_bytes(cfg)), torch.uint8, dev, stream)
+    _enqueue("moe_route_gated", dev, stream, _addr(x), _addr(router_w), _addr(router_bias),
+             _addr(balance_bias), gating.ref, _addr(idx), _addr(gates), _addr(logits),
+             ctypes.byref(cfg), _addr(workspace), workspace.numel())
+    return (idx, gates, logits) if with_logits else (idx, gates)
+
+
+def moe_forward_gated(x: torch.Tensor, router_w: torch.Tensor, bank: Bank, top_k: int, block: int,
+                      gating: Gating, shared: Optional[Bank] = None,
+                      router_bias: Optional[torch.Tensor] = None,
+                      balance_bias: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                      path: str = "auto", out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The whole layer with the gated choice of experts, through moe_forward_gated."""
+    dev = _place(x, router_w, router_bias, balance_bias, bank.w_gate_up, out, workspace)
+    _dev(x)
+    T, H = x.shape
+    E = router_w.shape[0]
+    I = bank.w_gate_up.shape[1] // 2
+    _flat(router_w, (E, H), torch.float32, "router_w")
+    _flat(router_bias, (E,), torch.float32, "router_bias")
+    _flat(balance_bias, (E,), torch.float32, "balance_bias")
+    _flat(out, (T, H), out_dtype, "out")
+    cfg = make_config(T, H, E, I, top_k, block, shared is not None, x.dtype, out_dtype, path)
+    bank.check(E, H, I, block)
+    if shared is not None:
+        shared.check(1, H, I, block)
+    if out is None:
+        out = _empty((T, H), out_dtype, dev, stream)
+    if workspace is None:
+        workspace = _empty(max(1, workspace_bytes(cfg)), torch.uint8, dev, stream)
+    _enqueue("moe_forward_gated", dev, stream, _addr(x), _addr(router_w), _addr(router_bias),
+             _addr(balance_bias), gating.ref, ctypes.byref(bank.c),
+             ctypes.byref(shared.c) if shared is not None else None, top_k, _addr(out),
+             ctypes.byref(cfg), _addr(workspace), workspace.numel(), None)
+    return out
+
+
+def linear_workspace_bytes(rows: int, out_features: int, in_features: int, x_is_codes: bool) -> int:
+    return int(load().moe_linear_workspace_bytes(rows, out_features, in_features,
+                                                 int(bool(x_is_codes))))
+
+
+def _linear(name, dev, stream, head, codes, w, w_scales, bias, M, K, out_dtype, out, workspace):
+    N = w.shape[0]
+    _flat(w, (N, K), torch.uint8, "w")
+    _flat(w_scales, (-(-N // 128), K // 128), torch.float32, "w_scales")
+    _flat(bias, (N,), torch.float32, "bias")
+    if out is None:
+        if out_dtype not in _DTYPES:
+            raise ValueError(f"unsupported dtype {out_dtype}")
+        out = _empty((M, N), out_dtype, dev, stream)
+        ld_out = N
+    else:
+        if out.dtype not in _DTYPES or tuple(out.shape) != (M, N):
+            raise ValueError(f"out must be a float32 or bfloat16 tensor of shape {(M, N)}")
+        ld_out = _rows(out, "out")
+        out_dtype = out.dtype
+    ws_bytes = load().moe_linear_workspace_bytes(M, N, K, codes)
+    if workspace is None and ws_bytes:
+        workspace = _empty(ws_bytes, torch.uint8, dev, stream)
+    _enqueue(name, dev, stream, *head, _addr(w), _addr(w_scales), _addr(bias), M, N, K, _addr(out),
+             ld_out, _DTYPES[out_dtype], _addr(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
+
+
+def moe_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """x [T][K] bf16 (rows may lie apart) times the transpose of a block-FP8
+    weight [N][K] (uint8, scales [ceil(N/128)][K/128] fp32), x quantised to
+    E4M3 per row and 128 columns, plus an optional fp32 bias."""
+    dev = _place(x, w, w_scales, bias, out, workspace)
+    ld = _rows(x, "x")
+    if x.dtype != torch.bfloat16:
+        raise ValueError("x must be bfloat16")
+    M, K = x.shape
+    return _linear("moe_linear", dev, stream, (_addr(x), ld), 0, w, w_scales, bias, M, K,
+                   out_dtype, out, workspace)
+
+
+def moe_linear_e4m3(codes: torch.Tensor, exps: torch.Tensor, w: torch.Tensor,
+                    w_scales: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                    out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_linear on activations that are quantised already (codes [T][K] and
+    exps [T][K/128] uint8, of moe_quantize_act_e4m3 or
+    moe_swiglu_quantize_e4m3)."""
+    dev = _place(codes, exps, w, w_scales, bias, out, workspace)
+    if codes.dim() != 2:
+        raise ValueError("codes must be 2-D")
+    M, K = codes.shape
+    _flat(codes, (M, K), torch.uint8, "codes")
+    _flat(exps, (M, K // 128), torch.uint8, "exps")
+    return _linear("moe_linear_e4m3", dev, stream, (_addr(codes), _addr(exps)), 1, w, w_scales,
+                   bias, M, K, out_dtype, out, workspace)
+
+
+def moe_swiglu_quantize_e4m3(gate_up: torch.Tensor, stream=None):
+    """silu(gate) * up of gate_up [T][2I] bf16 (rows may lie apart), quantised:
+    (E4M3 codes [T][I] uint8, E8M0 exponents [T][I/128] uint8)."""
+    dev = _place(gate_up)
+    ld = _rows(gate_up, "gate_up")
+    if gate_up.dtype != torch.bfloat16 or gate_up.shape[1] % 2:
+        raise ValueError("gate_up must be bfloat16 with an even number of columns")
+    T, I = gate_up.shape[0], gate_up.shape[1] // 2
+    codes = _empty((T, I), torch.uint8, dev, stream)
+    exps = _empty((T, I // 128), torch.uint8, dev, stream)
+    _enqueue("moe_swiglu_quantize_e4m3", dev, stream, _addr(gate_up), ld, T, I, _addr(codes),
+             _addr(exps))
+    return codes, exps

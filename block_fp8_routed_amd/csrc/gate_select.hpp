@@ -1,0 +1,34 @@
+// gate_select.hpp — the rule of one gated choice of experts and its order
+// keys. Internal to libmoe_fp8.so.
+#pragma once
+
+#include "device.hpp"
+
+namespace moe {
+
+constexpr int kMaxGroups = 64;  // a group's score is made by at least one lane
+constexpr float kMaskedLogit = -3.3e38f;  // at or below: the expert is masked
+
+// moe_gating, checked and completed for one layer.
+struct GateRule {
+  int experts, top_k;
+  int groups, per_group, top_groups, rank;
+  int lanes_per_group;  // largest power of two with lanes_per_group * groups <= 64
+  bool softmax, renorm;
+  float scale;
+};
+
+// fp64 values as unsigned keys in the same order (-0 as +0; no NaN comes
+// here). Every value's key is above the two marks.
+constexpr uint64_t kKeyAbsent = 0, kKeyMasked = 1;
+__device__ __forceinline__ uint64_t order_key(double c) {
+  const uint64_t b = (uint64_t)__double_as_longlong(c + 0.0);
+  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+}  // namespace moe

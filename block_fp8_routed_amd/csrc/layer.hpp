@@ -163,9 +163,11 @@ bool bank_ok(const moe_expert_bank* b);
 moe_status check_workspace(const Dims& d, void* ws, size_t bytes);
 // Router, selection and permutation (and the FP8 variant's activation
 // quantiser) for one call, with the optional phase events START and ROUTED.
+// gate (may be null): the gated choice, with its balance bias (may be null).
 moe_status enqueue_routing(const Dims& d, const void* x, const float* router_w,
                            const float* router_bias, const struct Work& w,
-                           const moe_phase_events* events, hipStream_t s);
+                           const moe_phase_events* events, hipStream_t s,
+                           const struct GateRule* gate = nullptr, const float* balance = nullptr);
 
 // Sum of region sizes; carve() lays them out in this order.
 size_t workspace_bytes(const Dims& d);
@@ -225,8 +227,16 @@ hipError_t launch_decode_fused(const Dims& d, const void* x, const float* router
                                hipStream_t s, KernelEvents ev);
 bool has_mfma_instance(const Dims& d);
 hipError_t launch_combine(const Dims& d, const Work& w, void* out, hipStream_t s);
-// x [T][H] bf16 -> E4M3 codes [T][H] and E8M0 exponents [T][H/128]
+// x [T][H] bf16 -> E4M3 codes [T][H] and E8M0 exponents [T][H/128]; rows of x
+// are ld elements apart (a multiple of 8; 0: H)
 hipError_t launch_quant_act(const void* x, int64_t T, int H, uint8_t* codes, uint8_t* exps,
-                            hipStream_t s);
+                            hipStream_t s, int64_t ld = 0);
+// The gated choice of experts (gate_select.hip): its checked rule, and its
+// launch on the router's partial logits (as launch_topk).
+struct GateRule;
+moe_status gate_rule(const moe_gating* g, int experts, int top_k, GateRule* r);
+hipError_t launch_gate_select(const Dims& d, const GateRule& r, const float* plog,
+                              const float* router_bias, const float* balance, int32_t* topk,
+                              float* gates, float* logits_out, int32_t* zero_word, hipStream_t s);
 
 }  // namespace moe

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "gate_select.hpp"
 #include "layer.hpp"
 
 namespace moe {
@@ -175,11 +176,17 @@ static bool rec(const moe_phase_events* ev, moe_phase p, hipStream_t s) {
 
 moe_status enqueue_routing(const Dims& d, const void* x, const float* router_w,
                            const float* router_bias, const Work& w, const moe_phase_events* events,
-                           hipStream_t s) {
+                           hipStream_t s, const GateRule* gate, const float* balance) {
   if (!rec(events, MOE_EV_START, s)) return MOE_ERR_HIP;
   if (launch_router(d, x, router_w, w, s) != hipSuccess) return MOE_ERR_HIP;
   const int tile_rows = d.mfma ? kMfmaBM : 0;
-  if (small_select_permute(d)) {
+  if (gate) {
+    if (launch_gate_select(d, *gate, w.logits, router_bias, balance, w.topk, w.gates, nullptr,
+                           w.meta + kMetaPermCounter, s) != hipSuccess)
+      return MOE_ERR_HIP;
+    if (!rec(events, MOE_EV_ROUTED, s)) return MOE_ERR_HIP;
+    if (launch_permute(d, w.topk, w, tile_rows, true, s) != hipSuccess) return MOE_ERR_HIP;
+  } else if (small_select_permute(d)) {
     // decode sizes: selection and permutation share one launch, so ROUTED
     // marks the end of the router logits here
     if (!rec(events, MOE_EV_ROUTED, s)) return MOE_ERR_HIP;
@@ -201,22 +208,25 @@ moe_status enqueue_routing(const Dims& d, const void* x, const float* router_w,
 
 using namespace moe;
 
-extern "C" {
-
-size_t moe_workspace_bytes(const moe_config* cfg) {
-  Dims d;
-  if (basic_dims(cfg, &d) != MOE_OK) return 0;
-  return workspace_bytes(d);
-}
-
-moe_status moe_forward(const void* x, const float* router_w, const float* router_bias,
-                       const moe_expert_bank* experts, const moe_expert_bank* shared,
-                       int32_t top_k, void* out, const moe_config* cfg, void* workspace,
-                       size_t workspace_bytes_, const moe_phase_events* events, void* stream) {
+static moe_status forward(const void* x, const float* router_w, const float* router_bias,
+                          const float* balance_bias, const moe_gating* gating, bool gated,
+                          const moe_expert_bank* experts, const moe_expert_bank* shared,
+                          int32_t top_k, void* out, const moe_config* cfg, void* workspace,
+                          size_t workspace_bytes_, const moe_phase_events* events, void* stream) {
   Dims d;
   moe_status st = basic_dims(cfg, &d);
   if (st != MOE_OK) return st;
   if (top_k != cfg->top_k) return MOE_ERR_SHAPE;
+  GateRule rule;
+  if (gated) {
+    st = gate_rule(gating, d.E, d.k, &rule);
+    if (st != MOE_OK) return st;
+    // the single-launch layer selects by the logits alone
+    if (cfg->path == MOE_PATH_GEMV_FUSED) return MOE_ERR_UNSUPPORTED;
+    // the gated choice is a launch of its own, which does not clear the
+    // fold's counters
+    d.fold_combine = false;
+  }
   if (!x || !router_w || !out || !bank_ok(experts)) return MOE_ERR_NULL;
   if (d.S && !bank_ok(shared)) return MOE_ERR_NULL;
   st = expert_family_ok(d);
@@ -243,7 +253,8 @@ moe_status moe_forward(const void* x, const float* router_w, const float* router
     if (!rec(events, MOE_EV_DOWN, s) || !rec(events, MOE_EV_END, s)) return MOE_ERR_HIP;
     return MOE_OK;
   }
-  st = enqueue_routing(d, x, router_w, router_bias, w, events, s);
+  st = enqueue_routing(d, x, router_w, router_bias, w, events, s, gated ? &rule : nullptr,
+                       balance_bias);
   if (st != MOE_OK) return st;
   const moe_expert_bank* sh = d.S ? shared : nullptr;
   const hipError_t e =
@@ -255,6 +266,55 @@ moe_status moe_forward(const void* x, const float* router_w, const float* router
   // (decode GEMV path: the down kernel has combined already)
   if (!d.fold_combine && launch_combine(d, w, out, s) != hipSuccess) return MOE_ERR_HIP;
   if (!rec(events, MOE_EV_END, s)) return MOE_ERR_HIP;
+  return MOE_OK;
+}
+
+extern "C" {
+
+size_t moe_workspace_bytes(const moe_config* cfg) {
+  Dims d;
+  if (basic_dims(cfg, &d) != MOE_OK) return 0;
+  return workspace_bytes(d);
+}
+
+moe_status moe_forward(const void* x, const float* router_w, const float* router_bias,
+                       const moe_expert_bank* experts, const moe_expert_bank* shared,
+                       int32_t top_k, void* out, const moe_config* cfg, void* workspace,
+                       size_t workspace_bytes_, const moe_phase_events* events, void* stream) {
+  return forward(x, router_w, router_bias, nullptr, nullptr, false, experts, shared, top_k, out,
+                 cfg, workspace, workspace_bytes_, events, stream);
+}
+
+moe_status moe_forward_gated(const void* x, const float* router_w, const float* router_bias,
+                             const float* balance_bias, const moe_gating* gating,
+                             const moe_expert_bank* experts, const moe_expert_bank* shared,
+                             int32_t top_k, void* out, const moe_config* cfg, void* workspace,
+                             size_t workspace_bytes_, const moe_phase_events* events,
+                             void* stream) {
+  return forward(x, router_w, router_bias, balance_bias, gating, true, experts, shared, top_k, out,
+                 cfg, workspace, workspace_bytes_, events, stream);
+}
+
+moe_status moe_route_gated(const void* x, const float* router_w, const float* router_bias,
+                           const float* balance_bias, const moe_gating* gating,
+                           int32_t* topk_idx, float* gates, float* logits, const moe_config* cfg,
+                           void* workspace, size_t workspace_bytes_, void* stream) {
+  Dims d;
+  moe_status st = basic_dims(cfg, &d);
+  if (st != MOE_OK) return st;
+  GateRule rule;
+  st = gate_rule(gating, d.E, d.k, &rule);
+  if (st != MOE_OK) return st;
+  if (!x || !router_w || !topk_idx || !gates) return MOE_ERR_NULL;
+  if (d.T == 0) return MOE_OK;
+  st = check_workspace(d, workspace, workspace_bytes_);
+  if (st != MOE_OK) return st;
+  const Work w = carve(d, workspace);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (launch_router(d, x, router_w, w, s) != hipSuccess) return MOE_ERR_HIP;
+  if (launch_gate_select(d, rule, w.logits, router_bias, balance_bias, topk_idx, gates, logits,
+                         nullptr, s) != hipSuccess)
+    return MOE_ERR_HIP;
   return MOE_OK;
 }
 

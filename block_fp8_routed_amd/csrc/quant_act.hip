@@ -29,14 +29,19 @@
 namespace moe {
 
 // thread i of the grid takes 16-byte chunk i (columns 8 (i % 16) .. + 7 of
-// block i / 16); chunks past the end repeat the last one and store nothing
+// block i / 16); chunks past the end repeat the last one and store nothing.
+// STRIDED: rows of per_row chunks, ld_chunks apart (else one after the other)
+template <bool STRIDED>
 __global__ __launch_bounds__(256) void quant_act_kernel(const uint4* __restrict__ x,
                                                        int64_t nblocks,
                                                        uint2* __restrict__ codes,
-                                                       uint8_t* __restrict__ exps) {
+                                                       uint8_t* __restrict__ exps, int per_row,
+                                                       int64_t ld_chunks) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t n = nblocks * (kActBlock / 8);
-  const uint4 w = x[i < n ? i : n - 1];
+  int64_t src = i < n ? i : n - 1;
+  if (STRIDED) src = src / per_row * ld_chunks + src % per_row;
+  const uint4 w = x[src];
   const uint32_t d[4] = {w.x, w.y, w.z, w.w};
   float v[8];
 #pragma unroll
@@ -58,11 +63,16 @@ __global__ __launch_bounds__(256) void quant_act_kernel(const uint4* __restrict_
 }
 
 hipError_t launch_quant_act(const void* x, int64_t T, int H, uint8_t* codes, uint8_t* exps,
-                            hipStream_t s) {
+                            hipStream_t s, int64_t ld) {
   const int64_t nb = T * (H / kActBlock);
   const int64_t chunks = nb * (kActBlock / 8);
-  quant_act_kernel<<<(unsigned)((chunks + 255) / 256), 256, 0, s>>>(
-      static_cast<const uint4*>(x), nb, reinterpret_cast<uint2*>(codes), exps);
+  const unsigned grid = (unsigned)((chunks + 255) / 256);
+  const uint4* src = static_cast<const uint4*>(x);
+  uint2* dst = reinterpret_cast<uint2*>(codes);
+  if (ld == 0 || ld == H)
+    quant_act_kernel<false><<<grid, 256, 0, s>>>(src, nb, dst, exps, H / 8, H / 8);
+  else
+    quant_act_kernel<true><<<grid, 256, 0, s>>>(src, nb, dst, exps, H / 8, ld / 8);
   return hipGetLastError();
 }
 

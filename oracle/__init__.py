@@ -12,6 +12,7 @@ from .moe_oracle import (  # noqa: F401
     e4m3fn_round,
     expert_matrices,
     gate_weights,
+    h_admissible_codes,
     h_admissible_deviation,
     h_band_width,
     moe_layer,
@@ -23,4 +24,12 @@ from .moe_oracle import (  # noqa: F401
     softmax,
     swiglu_expert,
     tie_flags,
+)
+from .dense_oracle import (  # noqa: F401
+    block_weights,
+    expert_scores,
+    gated_choice,
+    gated_layer,
+    linear_e4m3,
+    swiglu,
 )
