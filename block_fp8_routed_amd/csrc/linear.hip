@@ -38,6 +38,7 @@ struct LinearArgs {
   void* out;
   int64_t M, ld_out;
   int N, K;
+  bool vec4;  // four values of out from a feature that is a multiple of 4 are aligned
 };
 
 __device__ __forceinline__ i32x8_t operand(uint4 a, uint4 b) {
@@ -57,11 +58,12 @@ __device__ __forceinline__ f16x8_t widen(int lo, int hi) {
   return __builtin_bit_cast(f16x8_t, v);
 }
 
-// acc += s * 2^(scale - 127) * (A B over 128 k): lane l holds row l % 16 of
-// each operand and the 32 k of its quarter l / 16 (any 32, the same for both
-// operands); the result's column l % 16 (B's row) at rows 4 (l / 16) + v.
-// scale: the E8M0 byte of B's row; s: the weights' block scale, premultiplied
-// as block_scale() does.
+// One block's share acc += s * 2^(scale - 127) * (A B over 128 k), in two
+// steps: block_product (the matrix instructions) and add_block (scales and
+// sum). Lane l holds row l % 16 of each operand and the 32 k of its quarter
+// l / 16 (any 32, the same for both operands); the result's column l % 16 (B's
+// row) at rows 4 (l / 16) + v. Byte SEL of scale is the E8M0 byte of B's row;
+// s is the weights' block scale, premultiplied as block_scale() does.
 // A sum of 128 code products reaches 2^25 and the activations' scale 2^120, so
 // a factor is held back until s joins: the FP8 instruction's A operand has the
 // constant scale 2^-kHold; the fp16 form takes what is above 2^100 out of 2^e.
@@ -70,25 +72,49 @@ template <bool BF16>
 __device__ __forceinline__ float block_scale(float s) {
   return BF16 ? s * (float)(1 << kHold) : s;
 }
-template <bool BF16>
-__device__ __forceinline__ void mma128(f32x4& acc, const i32x8_t& a, const i32x8_t& b, int scale,
-                                       float s) {
+template <bool BF16, int SEL>
+__device__ __forceinline__ f32x4 block_product(const i32x8_t& a, const i32x8_t& b, int scale) {
   f32x4 d = {0.f, 0.f, 0.f, 0.f};
-  if (BF16) {
-    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, 127 - kHold, 0, scale);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = fmaf(s, d[v], acc[v]);
-    return;
-  }
+  if (BF16)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, 127 - kHold, SEL,
+                                                            scale);
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     d = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen(a[2 * j], a[2 * j + 1]),
                                                widen(b[2 * j], b[2 * j + 1]), d, 0, 0, 0);
-  const int e = scale - 127, e0 = e < 100 ? e : 100;
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ f32x4 block_product_sel(const i32x8_t& a, const i32x8_t& b, int scale,
+                                                   int sel) {  // sel: a constant once unrolled
+  switch (sel) {
+    case 0: return block_product<BF16, 0>(a, b, scale);
+    case 1: return block_product<BF16, 1>(a, b, scale);
+    case 2: return block_product<BF16, 2>(a, b, scale);
+    default: return block_product<BF16, 3>(a, b, scale);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void add_block(f32x4& acc, const f32x4& d, int scale, int sel, float s) {
+  if (BF16) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] = fmaf(s, d[v], acc[v]);
+    return;
+  }
+  const int e = (int)(((uint32_t)scale >> (8 * sel)) & 255u) - 127, e0 = e < 100 ? e : 100;
   const float se = __builtin_ldexpf(s, e - e0);
 #pragma unroll
   for (int v = 0; v < 4; ++v) acc[v] = fmaf(se, __builtin_ldexpf(d[v], e0), acc[v]);
 }
+
+// One byte of a buffer (0 past its range).
+__device__ __forceinline__ uint8_t buffer_ld1(__amdgpu_buffer_rsrc_t r, uint32_t voff,
+                                              uint32_t soff) {
+  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, voff, soff, 0);
+}
+
+// Keeps what uses v behind what stands before (no instruction).
+__device__ __forceinline__ void pin(f32x4& v) { asm volatile("" : "+v"(v)); }
 
 template <bool BF16>
 __device__ __forceinline__ void store_out(void* out, int64_t at, float v) {
@@ -96,6 +122,44 @@ __device__ __forceinline__ void store_out(void* out, int64_t at, float v) {
     reinterpret_cast<uint16_t*>(out)[at] = (uint16_t)f32_to_bf16_bits(v);
   else
     reinterpret_cast<float*>(out)[at] = v;
+}
+
+// Four consecutive features n .. n + 3 of one row (fewer at the end of N).
+template <bool BF16>
+__device__ __forceinline__ void store4(const LinearArgs& p, int64_t row, int n, f32x4 v) {
+  if (n >= p.N) return;
+  if (p.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] += p.bias[n + j < p.N ? n + j : p.N - 1];
+  }
+  const int64_t at = row * p.ld_out + n;
+  if (p.vec4 && n + 4 <= p.N) {
+    if (BF16)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + at) =
+          make_uint2(f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
+                     f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16);
+    else
+      *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p.out) + at) = v;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (n + j < p.N) store_out<BF16>(p.out, at + j, v[j]);
+}
+
+// Tile of workgroup b. Workgroups go round-robin over the eight XCDs, each
+// with an L2 of its own: XCD x takes a contiguous run of a raster that walks
+// bands of four feature tiles down the rows, so that the workgroups it runs
+// together share operands.
+__device__ __forceinline__ void linear_tile_of(int b, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int total = tiles_m * tiles_n, x = b % kXcdCount, i = b / kXcdCount;
+  const int q = total / kXcdCount, r = total % kXcdCount;
+  const int t = x * q + (x < r ? x : r) + i;
+  constexpr int kBand = 4;
+  const int per = kBand * tiles_m, band = t / per, in = t - band * per;
+  const int width = tiles_n - band * kBand < kBand ? tiles_n - band * kBand : kBand;
+  tm = in / width;
+  tn = band * kBand + in - tm * width;
 }
 
 // One wavefront per tile of 16 output features x 16 rows, operands straight
@@ -117,32 +181,225 @@ __global__ __launch_bounds__(256) void linear_tile16(LinearArgs p) {
   for (int kb = 0; kb < KB; ++kb) {
     const i32x8_t a = operand(ld16(wp + kb * kLinB), ld16(wp + kb * kLinB + 64));
     const i32x8_t b = operand(ld16(ap + kb * kLinB), ld16(ap + kb * kLinB + 64));
-    mma128<BF16>(acc, a, b, ep[kb], block_scale<BF16>(sp[kb]));
+    const int e = ep[kb];
+    add_block<BF16>(acc, block_product<BF16, 0>(a, b, e), e, 0, block_scale<BF16>(sp[kb]));
   }
-  if (m0 + l16 >= p.M) return;
+  if (m0 + l16 < p.M) store4<BF16>(p, mr, n0 + 4 * q, acc);
+}
+
+// Larger batches: a workgroup of WM x WN wavefronts computes TM rows x TN
+// output features, 128 k (one scale block) per stage. A stage's operands go
+// from global memory straight into one of two LDS buffers (buffer_load ...
+// lds: lane l of a wavefront's load fills its 16 bytes at the load's base +
+// 16 l), the next stage's while this one is multiplied; each wavefront waits
+// for its own loads before the barrier that ends the stage. The two buffers
+// are separate LDS objects, so that the compiler sees that loads into one
+// leave the other's fragments alone.
+//   LDS rows are 128 bytes; 16-byte chunk c of row r lies at slot
+// c ^ ((r >> 1) & 7), which spreads a fragment read (16 rows, one chunk) over
+// all banks. The swizzle is applied on the global side of the load.
+//   A wavefront multiplies FN tiles of 16 features with FM tiles of 16 rows.
+// Its rows' E8M0 bytes for a stage lie in LDS in the order in which a lane
+// needs them: byte j of lane l16 is row 16 j + l16, four tiles' bytes to the
+// dword, of which the instruction selects one.
+//   A wavefront's features lie inside one weight block, so one block scale
+// serves its stage; it is fetched a stage ahead.
+template <int TM, int TN, int WM, int WN, bool BF16>
+struct LinTile {
+  static constexpr int kThreads = 64 * WM * WN;
+  static constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
+  static constexpr int kStage = (TM + TN) * kLinB;
+  static constexpr int LA = TM * 8 / kThreads, LW = TN * 8 / kThreads;  // 16-byte loads a thread
+  static_assert(TM % (16 * WM) == 0 && TN % (16 * WN) == 0 && kLinB % (TN / WN) == 0, "tiles");
+  static_assert(LA * kThreads == TM * 8 && LW * kThreads == TN * 8, "loads");
+  static_assert(TM <= kThreads, "a thread per row for the exponents");
+};
+
+template <int TM, int TN, int WM, int WN, bool BF16>
+__device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_m, int tiles_n) {
+  using S = LinTile<TM, TN, WM, WN, BF16>;
+  constexpr int FM = S::FM, FN = S::FN;
+  __shared__ __attribute__((aligned(16))) uint8_t buf0[S::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t buf1[S::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t ex0[S::kThreads];
+  __shared__ __attribute__((aligned(16))) uint8_t ex1[S::kThreads];
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  int tm, tn;
+  linear_tile_of(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * TM;
+  const int n0 = tn * TN;
+  const int KB = p.K / kLinB;
+  const int mrows = p.M - m0 < TM ? (int)(p.M - m0) : TM;
+  const int nrows = p.N - n0 < TN ? p.N - n0 : TN;
+  const uint8_t* abase = p.codes + m0 * p.K;
+  const uint8_t* wbase = p.w + (size_t)n0 * p.K;
+  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(abase, (uint32_t)mrows * (uint32_t)p.K);
+  const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(wbase, (uint32_t)nrows * (uint32_t)p.K);
+  // Load i of this thread takes LDS chunk tid + kThreads i of the operand: a
+  // row kThreads / 8 further down each time, which leaves the swizzle alone.
+  // Rows past the end lie past the resource's range and read as zero.
+  const int r0 = tid >> 3;
+  const uint32_t off0 = (uint32_t)r0 * (uint32_t)p.K + 16 * ((tid & 7) ^ ((r0 >> 1) & 7));
+  const uint32_t step = (uint32_t)(S::kThreads / 8) * (uint32_t)p.K;
+  static_assert(S::kThreads / 8 % 16 == 0, "row step keeps the swizzle");
+  auto issue = [&](uint8_t* buf, int kb) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int n = n0 + 4 * q + v;
-    if (n < p.N) store_out<BF16>(p.out, mr * p.ld_out + n, acc[v] + (p.bias ? p.bias[n] : 0.f));
+    for (int i = 0; i < S::LA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, buf + 16 * S::kThreads * i + 1024 * wave, 16,
+                                               off0 + i * step, (uint32_t)(kb * kLinB), 0, 0);
+#pragma unroll
+    for (int i = 0; i < S::LW; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          wr, buf + TM * kLinB + 16 * S::kThreads * i + 1024 * wave, 16, off0 + i * step,
+          (uint32_t)(kb * kLinB), 0, 0);
+  };
+  // the exponent of row tid, stage kb; row t of the tile is row t % (16 FM) of
+  // wavefront row t / (16 FM)
+  const __amdgpu_buffer_rsrc_t er = buffer_rsrc(p.exps + m0 * KB, (uint32_t)mrows * (uint32_t)KB);
+  const uint32_t eoff = (uint32_t)tid * (uint32_t)KB;
+  const int eslot = (tid / (16 * FM)) * (16 * FM) + (tid & 15) * FM + (tid % (16 * FM)) / 16;
+  auto exponent = [&](int kb) {
+    return buffer_ld1(er, eoff, (uint32_t)kb);
+  };
+  const int nblk = (n0 + wn * 16 * FN) / kLinB, nblks = (p.N + kLinB - 1) / kLinB;
+  const float* sp = p.ws + (size_t)(nblk < nblks ? nblk : nblks - 1) * KB;
+
+  f32x4 acc[FN][FM];
+#pragma unroll
+  for (int n = 0; n < FN; ++n)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int sw = (l16 >> 1) & 7;  // fragment rows are multiples of 16 plus l16
+  const int abyte = (wm * 16 * FM + l16) * kLinB;
+  const int wbyte = TM * kLinB + (wn * 16 * FN + l16) * kLinB;
+  const int c0 = 16 * (q ^ sw), c1 = 16 * ((q + 4) ^ sw);
+  auto fragment = [&](const uint8_t* row) {
+    return operand(*reinterpret_cast<const uint4*>(row + c0),
+                   *reinterpret_cast<const uint4*>(row + c1));
+  };
+  auto compute = [&](const uint8_t* buf, const uint8_t* ex, float s) {
+    uint32_t ew[(FM + 3) / 4];
+    if constexpr (FM >= 4) {
+#pragma unroll
+      for (int j = 0; j < FM / 4; ++j)
+        ew[j] = *reinterpret_cast<const uint32_t*>(ex + wm * 16 * FM + l16 * FM + 4 * j);
+    } else {
+      ew[0] = 0;
+#pragma unroll
+      for (int j = 0; j < FM; ++j) ew[0] |= (uint32_t)ex[wm * 16 * FM + l16 * FM + j] << (8 * j);
+    }
+    i32x8_t w[FN];
+#pragma unroll
+    for (int n = 0; n < FN; ++n) w[n] = fragment(buf + wbyte + n * 16 * kLinB);
+    // Row tile m's products start as tile m - 1's are scaled and added: the
+    // additions of d[n] stand before the product that overwrites it, four
+    // products after the one they wait for. The barriers and pin() keep
+    // the compiler to this order (it would add a product right after its
+    // start, and gather fragments it has no registers for).
+    i32x8_t a = fragment(buf + abyte);
+    f32x4 d[FN];
+#pragma unroll
+    for (int m = 0; m < FM; ++m) {
+      i32x8_t next = a;
+      if (m + 1 < FM) next = fragment(buf + abyte + (m + 1) * 16 * kLinB);
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        if (m > 0) {
+          pin(d[n]);
+          add_block<BF16>(acc[n][m - 1], d[n], (int)ew[(m - 1) / 4], (m - 1) & 3, s);
+        }
+        d[n] = block_product_sel<BF16>(w[n], a, (int)ew[m / 4], m & 3);
+      }
+      a = next;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      add_block<BF16>(acc[n][FM - 1], d[n], (int)ew[(FM - 1) / 4], (FM - 1) & 3, s);
+  };
+  constexpr int kWaitVm0 = 0x0F70;  // s_waitcnt vmcnt(0)
+  float s = sp[0];
+  // one stage: start the next one's loads (past the end: the last one's
+  // again, not used), multiply, then let them be seen
+  auto stage = [&](const uint8_t* cur, const uint8_t* ecur, uint8_t* nxt, uint8_t* enxt, int kb) {
+    const int k1 = kb + 1 < KB ? kb + 1 : KB - 1;
+    const uint8_t e = exponent(k1);
+    const float s1 = sp[k1];
+    issue(nxt, k1);
+    __builtin_amdgcn_sched_barrier(0);
+    compute(cur, ecur, block_scale<BF16>(s));
+    s = s1;
+    enxt[eslot] = e;
+    __builtin_amdgcn_s_waitcnt(kWaitVm0);
+    __syncthreads();
+  };
+  issue(buf0, 0);
+  ex0[eslot] = exponent(0);
+  __builtin_amdgcn_s_waitcnt(kWaitVm0);
+  __syncthreads();
+  int kb = 0;
+#pragma unroll 1
+  for (; kb + 1 < KB; kb += 2) {
+    stage(buf0, ex0, buf1, ex1, kb);
+    stage(buf1, ex1, buf0, ex0, kb + 1);
   }
+  if (kb < KB) compute(buf0, ex0, block_scale<BF16>(s));
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int64_t row = m0 + wm * 16 * FM + 16 * m + l16;
+    if (row >= p.M) continue;
+#pragma unroll
+    for (int n = 0; n < FN; ++n)
+      store4<BF16>(p, row, n0 + wn * 16 * FN + 16 * n + 4 * q, acc[n][m]);
+  }
+}
+
+template <int TM, int TN, int WM, int WN, bool BF16>
+__global__ __launch_bounds__(64 * WM * WN) void linear_tile(LinearArgs p, int tiles_m,
+                                                           int tiles_n) {
+  linear_tile_body<TM, TN, WM, WN, BF16>(p, tiles_m, tiles_n);
 }
 
 static size_t al256(size_t n) { return (n + 255) / 256 * 256; }
 
+template <int TM, int TN, int WM, int WN, bool BF16>
+static void launch_tile(const LinearArgs& p, hipStream_t s) {
+  const int tm = (int)((p.M + TM - 1) / TM), tn = (p.N + TN - 1) / TN;
+  linear_tile<TM, TN, WM, WN, BF16><<<(unsigned)((int64_t)tm * tn), 64 * WM * WN, 0, s>>>(p, tm, tn);
+}
+
+template <bool BF16>
+static void launch_form(const LinearArgs& p, hipStream_t s) {
+  if (p.M <= 32) {
+    const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 15) / 16));
+    linear_tile16<BF16><<<grid, 256, 0, s>>>(p);
+    return;
+  }
+  const auto tiles = [&](int tm, int tn) {
+    return ((p.M + tm - 1) / tm) * (int64_t)((p.N + tn - 1) / tn);
+  };
+  if constexpr (BF16)
+    if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, BF16>(p, s);
+  launch_tile<128, 128, 2, 2, BF16>(p, s);
+}
+
 static hipError_t launch_linear(const LinearArgs& p, bool bf16, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 15) / 16));
   if (bf16)
-    linear_tile16<true><<<grid, 256, 0, s>>>(p);
+    launch_form<true>(p, s);
   else
-    linear_tile16<false><<<grid, 256, 0, s>>>(p);
+    launch_form<false>(p, s);
   return hipGetLastError();
 }
 
 static moe_status check_sizes(int64_t M, int32_t N, int32_t K) {
   if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_SHAPE;
   if (K % kLinB != 0) return MOE_ERR_UNSUPPORTED;
-  // the tiles' row index, and the quantiser's grid
-  if (M > (1 << 20) || M * (K / kLinB) >= ((int64_t)1 << 27)) return MOE_ERR_UNSUPPORTED;
+  // 32-bit offsets within a tile, the tiles' count, and the quantiser's grid
+  if (K > (1 << 22) || N > (1 << 24) || M > (1 << 20) ||
+      (M + 15) / 16 * ((N + 63) / 64) >= ((int64_t)1 << 31) || M * (K / kLinB) >= ((int64_t)1 << 27)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -168,6 +425,8 @@ static moe_status linear_call(const void* x, int64_t ld_x, LinearArgs p, moe_dty
     p.codes = codes;
     p.exps = exps;
   }
+  const size_t quad = out_dtype == MOE_BF16 ? 8 : 16;
+  p.vec4 = reinterpret_cast<uintptr_t>(p.out) % quad == 0 && p.ld_out % 4 == 0;
   return launch_linear(p, out_dtype == MOE_BF16, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -191,7 +450,7 @@ moe_status moe_linear(const void* x, int64_t ld_x, const uint8_t* w, const float
                       size_t workspace_bytes, void* stream) {
   if (!x || !w || !w_scales || !out) return MOE_ERR_NULL;
   const LinearArgs p{nullptr, nullptr, w,    w_scales,     bias,
-                     out,     rows,    ld_out, out_features, in_features};
+                     out,     rows,    ld_out, out_features, in_features, false};
   return linear_call(x, ld_x, p, out_dtype, workspace, workspace_bytes,
                      static_cast<hipStream_t>(stream));
 }
@@ -202,7 +461,8 @@ moe_status moe_linear_e4m3(const uint8_t* codes, const uint8_t* exps, const uint
                            moe_dtype out_dtype, void* workspace, size_t workspace_bytes,
                            void* stream) {
   if (!codes || !exps || !w || !w_scales || !out) return MOE_ERR_NULL;
-  const LinearArgs p{codes, exps, w, w_scales, bias, out, rows, ld_out, out_features, in_features};
+  const LinearArgs p{codes, exps, w,      w_scales,     bias,        out,
+                     rows,  ld_out, out_features, in_features, false};
   return linear_call(nullptr, 0, p, out_dtype, workspace, workspace_bytes,
                      static_cast<hipStream_t>(stream));
 }
