@@ -484,25 +484,27 @@ _UNREAD = 256  # address given for an empty tensor, whose memory no call touches
 
 def _place(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> torch.device:
     dev = first.device
-    for t in (first, *rest):
-        if t is not None and (t.device != dev or not t.is_cuda):
+    for t in rest:
+        if t is not None and t.device != dev:
             raise ValueError("tensors must be on one GPU")
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on one GPU")
     return dev
 
 
 def _rows(t: torch.Tensor, what: str) -> int:
     """Distance in elements between the rows of a 2-D tensor with unit column
     stride (columns broadcast or out of order are refused)."""
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
-        raise ValueError(f"{what} must be 2-D with contiguous rows")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    return t.stride(0)
+    if t.dim() == 2:
+        ld, step = t.stride()
+        rows, cols = t.shape
+        if step == 1 or cols <= 1:
+            return ld if rows > 1 else cols
+    raise ValueError(f"{what} must be 2-D with contiguous rows")
 
 
 def _flat(t: Optional[torch.Tensor], shape, dtype, what: str):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)
-                          or not t.is_contiguous()):
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
@@ -511,23 +513,24 @@ def _addr(t: Optional[torch.Tensor]):
 
 
 def _empty(shape, dtype, dev, stream):
-    if stream is None:
-        if dev.index == torch.cuda.current_device():
-            return torch.empty(shape, dtype=dtype, device=dev)
-        stream = torch.cuda.current_stream(dev)
+    if stream is None:  # the device's current stream
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _enqueue(name: str, dev: torch.device, stream, *args):
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    fn = getattr(load(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, stream.cuda_stream)
+    """Calls the C function on the tensors' device and the given or that
+    device's current stream. (The raw handle is what current_stream() wraps;
+    building the wrapper takes as long as the rest of a small call's checks.)"""
+    fn = getattr(_lib or load(), name)
+    index = dev.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        st = fn(*args, s)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
+            st = fn(*args, s)
     if st != MOE_OK:
         raise MoeError(st, name)
 

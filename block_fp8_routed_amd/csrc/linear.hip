@@ -21,6 +21,7 @@
 // Weights are the instruction's A operand, so that a lane ends with four
 // consecutive output features of one row.
 #include "device.hpp"
+#include "e4m3_round.hpp"
 #include "layer.hpp"
 
 namespace moe {
@@ -30,6 +31,8 @@ constexpr int kLinB = 128;  // columns per scale block
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 struct LinearArgs {
+  const uint16_t* x;     // [M] rows of K bf16, ld_x apart, or null: codes and exps
+  int64_t ld_x;
   const uint8_t* codes;  // [M][K]
   const uint8_t* exps;   // [M][K/128]
   const uint8_t* w;      // [N][K]
@@ -162,29 +165,137 @@ __device__ __forceinline__ void linear_tile_of(int b, int tiles_m, int tiles_n, 
   tn = band * kBand + in - tm * width;
 }
 
-// One wavefront per tile of 16 output features x 16 rows, operands straight
-// from global memory.
-template <bool BF16>
-__global__ __launch_bounds__(256) void linear_tile16(LinearArgs p) {
-  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 16;
-  const int64_t m0 = (int64_t)blockIdx.y * 16;
-  if (n0 >= p.N) return;
-  const int nr = n0 + l16 < p.N ? n0 + l16 : p.N - 1;
-  const int64_t mr = m0 + l16 < p.M ? m0 + l16 : p.M - 1;
-  const int KB = p.K / kLinB;
-  const uint8_t* wp = p.w + (size_t)nr * p.K + 16 * q;
-  const uint8_t* ap = p.codes + (size_t)mr * p.K + 16 * q;
-  const uint8_t* ep = p.exps + (size_t)mr * KB;
-  const float* sp = p.ws + (size_t)(n0 / kLinB) * KB;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int kb = 0; kb < KB; ++kb) {
-    const i32x8_t a = operand(ld16(wp + kb * kLinB), ld16(wp + kb * kLinB + 64));
-    const i32x8_t b = operand(ld16(ap + kb * kLinB), ld16(ap + kb * kLinB + 64));
-    const int e = ep[kb];
-    add_block<BF16>(acc, block_product<BF16, 0>(a, b, e), e, 0, block_scale<BF16>(sp[kb]));
+// Small batches: the weights' bytes bound the product, so it is laid out as a
+// stream of them. A workgroup takes 16 FN output features and up to 16 FM
+// rows; its W wavefronts take every W-th block of K, weights and activations
+// straight from global memory into operand registers (a load instruction
+// covers 64 bytes of each of 16 weight rows), U blocks requested together; the
+// partial sums meet in LDS and are added in wavefront order. The products are
+// the exact fp16 ones for both output types: the matrix units have room to
+// spare here.
+//   XQ: the activations are bf16 rows of x, quantised as they are read: a
+// lane holds 32 of a row's 128 columns, the row's four lanes agree on the
+// largest magnitude, and the conversion instruction does the rest. Each
+// workgroup repeats that work for its own features, which up to 16 rows is
+// cheaper than a launch of its own (measured below).
+__device__ __forceinline__ i32x8_t quantised_operand(const uint4 (&v)[4], int& e) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, bf16x8_max_abs(v[i]));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+  e = act_exponent(__uint_as_float(m << 16));
+  i32x8_t o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint2 q = e4m3x8_of_bf16(v[i], e);
+    o[2 * i] = (int)q.x;
+    o[2 * i + 1] = (int)q.y;
   }
-  if (m0 + l16 < p.M) store4<BF16>(p, mr, n0 + 4 * q, acc);
+  e += 127;
+  return o;
+}
+
+template <int FM, int FN, int W, int U, bool XQ, bool BF16>
+__device__ __forceinline__ void linear_rows_body(const LinearArgs& p) {
+  __shared__ f32x4 red[W][FM * FN][64];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16 * FN;
+  const int64_t m0 = (int64_t)blockIdx.y * 16 * FM;
+  const int KB = p.K / kLinB;
+  const uint8_t* wp[FN];
+  const float* sp[FN];
+#pragma unroll
+  for (int n = 0; n < FN; ++n) {
+    const int nt = n0 + 16 * n < p.N ? n0 + 16 * n : n0;  // a tile past the end repeats the first
+    const int r = nt + l16 < p.N ? nt + l16 : p.N - 1;
+    wp[n] = p.w + (size_t)r * p.K + 16 * q;
+    sp[n] = p.ws + (size_t)(nt / kLinB) * KB;
+  }
+  const uint8_t* ap[FM];
+  const uint8_t* ep[FM];
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int64_t r = m0 + 16 * m + l16 < p.M ? m0 + 16 * m + l16 : p.M - 1;
+    if (XQ) {
+      ap[m] = reinterpret_cast<const uint8_t*>(p.x + r * p.ld_x + 16 * q);
+    } else {
+      ap[m] = p.codes + (size_t)r * p.K + 16 * q;
+      ep[m] = p.exps + (size_t)r * KB;
+    }
+  }
+  f32x4 acc[FN][FM];
+#pragma unroll
+  for (int n = 0; n < FN; ++n)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // U blocks a round; blocks past the end repeat the last one with scale 0
+  for (int kb0 = wave; kb0 < KB; kb0 += W * U) {
+    uint4 w[U][FN][2], av[U][FM][XQ ? 4 : 2];
+    int ev[U][FM];
+    float s[U][FN];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k0 = kb0 + u * W, kb = k0 < KB ? k0 : KB - 1;
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        w[u][n][0] = ld16(wp[n] + (size_t)kb * kLinB);
+        w[u][n][1] = ld16(wp[n] + (size_t)kb * kLinB + 64);
+        s[u][n] = k0 < KB ? sp[n][kb] : 0.f;
+      }
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        if (XQ) {
+          const uint8_t* x = ap[m] + (size_t)kb * (2 * kLinB);
+          av[u][m][0] = ld16(x);
+          av[u][m][1] = ld16(x + 16);
+          av[u][m][2] = ld16(x + 128);
+          av[u][m][3] = ld16(x + 144);
+        } else {
+          av[u][m][0] = ld16(ap[m] + (size_t)kb * kLinB);
+          av[u][m][1] = ld16(ap[m] + (size_t)kb * kLinB + 64);
+          ev[u][m] = ep[m][kb];
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        i32x8_t a;
+        int e;
+        if constexpr (XQ) {
+          a = quantised_operand(av[u][m], e);
+        } else {
+          a = operand(av[u][m][0], av[u][m][1]);
+          e = ev[u][m];
+        }
+#pragma unroll
+        for (int n = 0; n < FN; ++n)
+          add_block<false>(acc[n][m],
+                           block_product<false, 0>(operand(w[u][n][0], w[u][n][1]), a, e), e, 0,
+                           s[u][n]);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < FN; ++n)
+#pragma unroll
+    for (int m = 0; m < FM; ++m) red[wave][n * FM + m][lane] = acc[n][m];
+  __syncthreads();
+  for (int t = wave; t < FM * FN; t += W) {
+    f32x4 v = red[0][t][lane];
+#pragma unroll
+    for (int i = 1; i < W; ++i) v += red[i][t][lane];
+    const int64_t row = m0 + 16 * (t % FM) + l16;
+    if (row < p.M) store4<BF16>(p, row, n0 + 16 * (t / FM) + 4 * q, v);
+  }
+}
+
+template <int FM, int FN, int W, int U, bool XQ, bool BF16>
+__global__ __launch_bounds__(64 * W) void linear_rows(LinearArgs p) {
+  linear_rows_body<FM, FN, W, U, XQ, BF16>(p);
 }
 
 // Larger batches: a workgroup of WM x WN wavefronts computes TM rows x TN
@@ -371,16 +482,26 @@ static void launch_tile(const LinearArgs& p, hipStream_t s) {
   linear_tile<TM, TN, WM, WN, BF16><<<(unsigned)((int64_t)tm * tn), 64 * WM * WN, 0, s>>>(p, tm, tn);
 }
 
+template <int FM, int FN, int W, int U, bool XQ, bool BF16>
+static void launch_rows(const LinearArgs& p, hipStream_t s) {
+  const dim3 grid((unsigned)((p.N + 16 * FN - 1) / (16 * FN)),
+                  (unsigned)((p.M + 16 * FM - 1) / (16 * FM)));
+  linear_rows<FM, FN, W, U, XQ, BF16><<<grid, 64 * W, 0, s>>>(p);
+}
+
+// Whether the product quantises bf16 rows itself (one launch).
+static bool quantises_inside(int64_t M) { return M <= 16; }
+
 template <bool BF16>
 static void launch_form(const LinearArgs& p, hipStream_t s) {
-  if (p.M <= 32) {
-    const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 15) / 16));
-    linear_tile16<BF16><<<grid, 256, 0, s>>>(p);
-    return;
-  }
+  if (p.M <= 16) return p.x ? launch_rows<1, 1, 8, 2, true, BF16>(p, s)
+                            : launch_rows<1, 1, 8, 4, false, BF16>(p, s);
   const auto tiles = [&](int tm, int tn) {
     return ((p.M + tm - 1) / tm) * (int64_t)((p.N + tn - 1) / tn);
   };
+  if (p.M <= 32) return launch_rows<2, 1, 8, 2, false, BF16>(p, s);
+  if (p.M <= 64) return launch_rows<4, 1, 8, 2, false, BF16>(p, s);
+  if (p.M <= 128 && tiles(128, 128) < 128) return launch_rows<8, 1, 8, 1, false, BF16>(p, s);
   if constexpr (BF16)
     if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, BF16>(p, s);
   launch_tile<128, 128, 2, 2, BF16>(p, s);
@@ -403,25 +524,27 @@ static moe_status check_sizes(int64_t M, int32_t N, int32_t K) {
   return MOE_OK;
 }
 
-static moe_status linear_call(const void* x, int64_t ld_x, LinearArgs p, moe_dtype out_dtype,
-                              void* workspace, size_t workspace_bytes, hipStream_t s) {
+static moe_status linear_call(LinearArgs p, moe_dtype out_dtype, void* workspace,
+                              size_t workspace_bytes, hipStream_t s) {
   const moe_status st = check_sizes(p.M, p.N, p.K);
   if (st != MOE_OK) return st;
   if (out_dtype != MOE_F32 && out_dtype != MOE_BF16) return MOE_ERR_SHAPE;
-  if (p.ld_out < p.N || (x && ld_x < p.K)) return MOE_ERR_SHAPE;
+  if (p.ld_out < p.N || (p.x && p.ld_x < p.K)) return MOE_ERR_SHAPE;
   if (p.M == 0) return MOE_OK;
   const auto odd16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 != 0; };
-  if (odd16(x) || odd16(p.codes) || odd16(p.w) || (x && ld_x % 8 != 0)) return MOE_ERR_UNSUPPORTED;
-  const size_t need = moe_linear_workspace_bytes(p.M, p.N, p.K, x ? 0 : 1);
+  if (odd16(p.x) || odd16(p.codes) || odd16(p.w) || (p.x && p.ld_x % 8 != 0))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t need = moe_linear_workspace_bytes(p.M, p.N, p.K, p.x ? 0 : 1);
   if (need > 0) {
     if (!workspace) return MOE_ERR_NULL;
     if (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
       return MOE_ERR_WORKSPACE;
   }
-  if (x) {
+  if (p.x && !quantises_inside(p.M)) {
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* exps = codes + al256((size_t)p.M * p.K);
-    if (launch_quant_act(x, p.M, p.K, codes, exps, s, ld_x) != hipSuccess) return MOE_ERR_HIP;
+    if (launch_quant_act(p.x, p.M, p.K, codes, exps, s, p.ld_x) != hipSuccess) return MOE_ERR_HIP;
+    p.x = nullptr;
     p.codes = codes;
     p.exps = exps;
   }
@@ -439,9 +562,8 @@ extern "C" {
 size_t moe_linear_workspace_bytes(int64_t rows, int32_t out_features, int32_t in_features,
                                   int32_t x_is_codes) {
   if (check_sizes(rows, out_features, in_features) != MOE_OK || rows == 0) return 0;
-  return x_is_codes ? 0
-                    : al256((size_t)rows * in_features) +
-                          al256((size_t)rows * (in_features / kLinB));
+  if (x_is_codes || quantises_inside(rows)) return 0;
+  return al256((size_t)rows * in_features) + al256((size_t)rows * (in_features / kLinB));
 }
 
 moe_status moe_linear(const void* x, int64_t ld_x, const uint8_t* w, const float* w_scales,
@@ -449,10 +571,18 @@ moe_status moe_linear(const void* x, int64_t ld_x, const uint8_t* w, const float
                       void* out, int64_t ld_out, moe_dtype out_dtype, void* workspace,
                       size_t workspace_bytes, void* stream) {
   if (!x || !w || !w_scales || !out) return MOE_ERR_NULL;
-  const LinearArgs p{nullptr, nullptr, w,    w_scales,     bias,
-                     out,     rows,    ld_out, out_features, in_features, false};
-  return linear_call(x, ld_x, p, out_dtype, workspace, workspace_bytes,
-                     static_cast<hipStream_t>(stream));
+  LinearArgs p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.ld_x = ld_x;
+  p.w = w;
+  p.ws = w_scales;
+  p.bias = bias;
+  p.out = out;
+  p.M = rows;
+  p.ld_out = ld_out;
+  p.N = out_features;
+  p.K = in_features;
+  return linear_call(p, out_dtype, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_linear_e4m3(const uint8_t* codes, const uint8_t* exps, const uint8_t* w,
@@ -461,10 +591,18 @@ moe_status moe_linear_e4m3(const uint8_t* codes, const uint8_t* exps, const uint
                            moe_dtype out_dtype, void* workspace, size_t workspace_bytes,
                            void* stream) {
   if (!codes || !exps || !w || !w_scales || !out) return MOE_ERR_NULL;
-  const LinearArgs p{codes, exps, w,      w_scales,     bias,        out,
-                     rows,  ld_out, out_features, in_features, false};
-  return linear_call(nullptr, 0, p, out_dtype, workspace, workspace_bytes,
-                     static_cast<hipStream_t>(stream));
+  LinearArgs p{};
+  p.codes = codes;
+  p.exps = exps;
+  p.w = w;
+  p.ws = w_scales;
+  p.bias = bias;
+  p.out = out;
+  p.M = rows;
+  p.ld_out = ld_out;
+  p.N = out_features;
+  p.K = in_features;
+  return linear_call(p, out_dtype, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"

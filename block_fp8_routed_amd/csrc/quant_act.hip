@@ -13,14 +13,12 @@
 // block-scaled FP8 matrix instructions take (E8M0), so the scale can ride in
 // the instruction itself.
 //
-// x * 2^-e is exact in fp32 (a bf16 value times a power of two), except
-// below 2^-126, where fp32 rounds; such values are far below half of
-// E4M3's smallest subnormal (2^-10) and give a zero code either way, so
+// The conversion instruction takes 2^e itself and rounds x * 2^-e once, so
 // each code is decided exactly as an exact-arithmetic rounding would.
 //
 // Sixteen lanes per block (a DPP row): lane L of a row takes columns 8L ..
 // 8L + 7 with one 16-byte load, and the block's largest magnitude comes from
-// a four-step DPP maximum within the row over the lanes' fp32 bit patterns
+// a four-step DPP maximum within the row over the lanes' bf16 bit patterns
 // (non-negative floats order as unsigned integers).
 #include "device.hpp"
 #include "e4m3_round.hpp"
@@ -30,49 +28,38 @@ namespace moe {
 
 // thread i of the grid takes 16-byte chunk i (columns 8 (i % 16) .. + 7 of
 // block i / 16); chunks past the end repeat the last one and store nothing.
-// STRIDED: rows of per_row chunks, ld_chunks apart (else one after the other)
+// STRIDED: rows of per_row chunks, ld_chunks apart (else one after the other).
+// x is read and the codes written once each, non-temporally.
 template <bool STRIDED>
-__global__ __launch_bounds__(256) void quant_act_kernel(const uint4* __restrict__ x,
-                                                       int64_t nblocks,
+__global__ __launch_bounds__(256) void quant_act_kernel(const uint4* __restrict__ x, uint32_t n,
                                                        uint2* __restrict__ codes,
                                                        uint8_t* __restrict__ exps, int per_row,
-                                                       int64_t ld_chunks) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t n = nblocks * (kActBlock / 8);
-  int64_t src = i < n ? i : n - 1;
-  if (STRIDED) src = src / per_row * ld_chunks + src % per_row;
-  const uint4 w = x[src];
-  const uint32_t d[4] = {w.x, w.y, w.z, w.w};
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = bf16_lo(d[j]);
-    v[2 * j + 1] = bf16_hi(d[j]);
+                                                       FastDiv by_row, int64_t ld_chunks) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x, c = i < n ? i : n - 1;
+  int64_t src = c;
+  if (STRIDED) {
+    const uint32_t row = by_row.div(c);
+    src = row * ld_chunks + (c - row * (uint32_t)per_row);
   }
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(fabsf(v[j])));
-  const int e = act_exponent(__uint_as_float(row16_max_u32(m)));
-  uint32_t c[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) c[j] = e4m3_rne(__builtin_ldexpf(v[j], -e));
+  const uint4 w = ld16_nt(x + src);
+  const int e = act_exponent(__uint_as_float(row16_max_u32(bf16x8_max_abs(w)) << 16));
   if (i >= n) return;
-  codes[i] = make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24),
-                        c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
+  const uint2 q = e4m3x8_of_bf16(w, e);
+  codes[i] = q;
   if ((i & 15) == 0) exps[i >> 4] = (uint8_t)(e + 127);
 }
 
 hipError_t launch_quant_act(const void* x, int64_t T, int H, uint8_t* codes, uint8_t* exps,
                             hipStream_t s, int64_t ld) {
-  const int64_t nb = T * (H / kActBlock);
-  const int64_t chunks = nb * (kActBlock / 8);
-  const unsigned grid = (unsigned)((chunks + 255) / 256);
+  const uint32_t n = (uint32_t)(T * (H / 8));  // below 2^31 (the callers' limit on blocks)
+  const unsigned grid = (n + 255) / 256;
   const uint4* src = static_cast<const uint4*>(x);
   uint2* dst = reinterpret_cast<uint2*>(codes);
+  const FastDiv by_row = FastDiv::of((uint32_t)(H / 8));
   if (ld == 0 || ld == H)
-    quant_act_kernel<false><<<grid, 256, 0, s>>>(src, nb, dst, exps, H / 8, H / 8);
+    quant_act_kernel<false><<<grid, 256, 0, s>>>(src, n, dst, exps, H / 8, by_row, H / 8);
   else
-    quant_act_kernel<true><<<grid, 256, 0, s>>>(src, nb, dst, exps, H / 8, ld / 8);
+    quant_act_kernel<true><<<grid, 256, 0, s>>>(src, n, dst, exps, H / 8, by_row, ld / 8);
   return hipGetLastError();
 }
 
