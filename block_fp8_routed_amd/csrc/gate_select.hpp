@@ -14,6 +14,11 @@ struct GateRule {
   int experts, top_k;
   int groups, per_group, top_groups, rank;
   int lanes_per_group;  // largest power of two with lanes_per_group * groups <= 64
+  int nv;               // experts per lane, consecutive ones
+  bool vec;             // a lane's logits can be read with vector loads
+  bool fast;            // every lane lies in one group: fp32 keys first
+  int group_lanes;      // (fast) lanes of a group, and one over it
+  float inv_group_lanes;
   bool softmax, renorm;
   float scale;
 };
@@ -24,6 +29,9 @@ constexpr uint64_t kKeyAbsent = 0, kKeyMasked = 1;
 __device__ __forceinline__ uint64_t order_key(double c) {
   const uint64_t b = (uint64_t)__double_as_longlong(c + 0.0);
   return (b >> 63) ? ~b : b | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double key_value(uint64_t k) {
+  return __longlong_as_double((long long)((k >> 63) ? k & 0x7fffffffffffffffull : ~k));
 }
 __device__ __forceinline__ uint64_t readlane_u64(uint64_t v, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)v, lane);
