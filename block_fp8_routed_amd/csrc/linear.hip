@@ -110,10 +110,12 @@ __device__ __forceinline__ void add_block(f32x4& acc, const f32x4& d, int scale,
   for (int v = 0; v < 4; ++v) acc[v] = fmaf(se, __builtin_ldexpf(d[v], e0), acc[v]);
 }
 
-// One byte of a buffer (0 past its range).
-__device__ __forceinline__ uint8_t buffer_ld1(__amdgpu_buffer_rsrc_t r, uint32_t voff,
-                                              uint32_t soff) {
-  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(r, voff, soff, 0);
+// One byte, or an aligned dword, of a buffer (0 past its range).
+__device__ __forceinline__ uint32_t buffer_ld1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+}
+__device__ __forceinline__ uint32_t buffer_ld4(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
 }
 
 // Keeps what uses v behind what stands before (no instruction).
@@ -300,40 +302,65 @@ __global__ __launch_bounds__(64 * W) void linear_rows(LinearArgs p) {
 
 // Larger batches: a workgroup of WM x WN wavefronts computes TM rows x TN
 // output features, 128 k (one scale block) per stage. A stage's operands go
-// from global memory straight into one of two LDS buffers (buffer_load ...
-// lds: lane l of a wavefront's load fills its 16 bytes at the load's base +
-// 16 l), the next stage's while this one is multiplied; each wavefront waits
-// for its own loads before the barrier that ends the stage. The two buffers
-// are separate LDS objects, so that the compiler sees that loads into one
-// leave the other's fragments alone.
+// from global memory straight into one of NST LDS buffers (buffer_load ... lds:
+// lane l of a wavefront's load fills its 16 bytes at the load's base + 16 l),
+// NST - 1 stages ahead of the one that is multiplied.
 //   LDS rows are 128 bytes; 16-byte chunk c of row r lies at slot
 // c ^ ((r >> 1) & 7), which spreads a fragment read (16 rows, one chunk) over
 // all banks. The swizzle is applied on the global side of the load.
 //   A wavefront multiplies FN tiles of 16 features with FM tiles of 16 rows.
-// Its rows' E8M0 bytes for a stage lie in LDS in the order in which a lane
+// The E8M0 bytes of kChunk stages lie in LDS in the order in which a lane
 // needs them: byte j of lane l16 is row 16 j + l16, four tiles' bytes to the
-// dword, of which the instruction selects one.
-//   A wavefront's features lie inside one weight block, so one block scale
-// serves its stage; it is fetched a stage ahead.
-template <int TM, int TN, int WM, int WN, bool BF16>
+// dword, of which the instruction selects one. A wavefront's features lie
+// inside one weight block, so one block scale serves its stage.
+template <int TM, int TN, int WM, int WN, int NST>
 struct LinTile {
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
   static constexpr int kStage = (TM + TN) * kLinB;
   static constexpr int LA = TM * 8 / kThreads, LW = TN * 8 / kThreads;  // 16-byte loads a thread
+  static constexpr int kLoads = LA + LW;
+  static constexpr int kChunk = 32;  // stages whose scales are held
+  static constexpr int kBlocks = (TN + kLinB - 1) / kLinB;
   static_assert(TM % (16 * WM) == 0 && TN % (16 * WN) == 0 && kLinB % (TN / WN) == 0, "tiles");
   static_assert(LA * kThreads == TM * 8 && LW * kThreads == TN * 8, "loads");
-  static_assert(TM <= kThreads, "a thread per row for the exponents");
+  static_assert(kThreads / 8 % 16 == 0, "a load's row step keeps the swizzle");
+  static_assert(NST >= 2 && NST <= 4 && (NST - 2) * kLoads <= 63, "loads in flight are counted in six bits");
 };
 
-template <int TM, int TN, int WM, int WN, bool BF16>
+// One 16-byte load of each lane into LDS, at lds + 16 lane. It is written as an
+// instruction of its own because the compiler, for the builtin, waits for every
+// such load in flight before the next LDS read, which would undo the ring; the
+// waits are the ring's own (wait_loads). It has no register output. A byte past
+// the resource's range is read as zero.
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, u32x4_t rsrc,
+                                            uint32_t soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
+      : "memory", "m0");
+}
+__device__ __forceinline__ u32x4_t raw_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, 0x00020000u};
+}
+// until at most N of the wavefront's loads are in flight (they end in order)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0f70);
+  asm volatile("" ::: "memory");
+}
+
+template <int TM, int TN, int WM, int WN, int NST, bool BF16>
 __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_m, int tiles_n) {
-  using S = LinTile<TM, TN, WM, WN, BF16>;
-  constexpr int FM = S::FM, FN = S::FN;
-  __shared__ __attribute__((aligned(16))) uint8_t buf0[S::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t buf1[S::kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t ex0[S::kThreads];
-  __shared__ __attribute__((aligned(16))) uint8_t ex1[S::kThreads];
+  using S = LinTile<TM, TN, WM, WN, NST>;
+  constexpr int FM = S::FM, FN = S::FN, kChunk = S::kChunk;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[NST * S::kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t ex[kChunk * TM];
+  __shared__ float sc[S::kBlocks * kChunk];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -344,38 +371,64 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
   const int KB = p.K / kLinB;
   const int mrows = p.M - m0 < TM ? (int)(p.M - m0) : TM;
   const int nrows = p.N - n0 < TN ? p.N - n0 : TN;
-  const uint8_t* abase = p.codes + m0 * p.K;
-  const uint8_t* wbase = p.w + (size_t)n0 * p.K;
-  const __amdgpu_buffer_rsrc_t ar = buffer_rsrc(abase, (uint32_t)mrows * (uint32_t)p.K);
-  const __amdgpu_buffer_rsrc_t wr = buffer_rsrc(wbase, (uint32_t)nrows * (uint32_t)p.K);
+  const u32x4_t ar = raw_rsrc(p.codes + m0 * p.K, (uint32_t)mrows * (uint32_t)p.K);
+  const u32x4_t wr = raw_rsrc(p.w + (size_t)n0 * p.K, (uint32_t)nrows * (uint32_t)p.K);
   // Load i of this thread takes LDS chunk tid + kThreads i of the operand: a
   // row kThreads / 8 further down each time, which leaves the swizzle alone.
   // Rows past the end lie past the resource's range and read as zero.
   const int r0 = tid >> 3;
   const uint32_t off0 = (uint32_t)r0 * (uint32_t)p.K + 16 * ((tid & 7) ^ ((r0 >> 1) & 7));
   const uint32_t step = (uint32_t)(S::kThreads / 8) * (uint32_t)p.K;
-  static_assert(S::kThreads / 8 % 16 == 0, "row step keeps the swizzle");
-  auto issue = [&](uint8_t* buf, int kb) {
+  const uint32_t lds0 =
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)ring + 1024 * wave;
+  auto issue = [&](int kb) {
+    const uint32_t at = lds0 + (uint32_t)(kb % NST) * S::kStage, k = (uint32_t)(kb * kLinB);
 #pragma unroll
     for (int i = 0; i < S::LA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, buf + 16 * S::kThreads * i + 1024 * wave, 16,
-                                               off0 + i * step, (uint32_t)(kb * kLinB), 0, 0);
+      load_to_lds(at + 16 * S::kThreads * i, off0 + i * step, ar, k);
 #pragma unroll
     for (int i = 0; i < S::LW; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wr, buf + TM * kLinB + 16 * S::kThreads * i + 1024 * wave, 16, off0 + i * step,
-          (uint32_t)(kb * kLinB), 0, 0);
+      load_to_lds(at + TM * kLinB + 16 * S::kThreads * i, off0 + i * step, wr, k);
   };
-  // the exponent of row tid, stage kb; row t of the tile is row t % (16 FM) of
-  // wavefront row t / (16 FM)
+  // Scales of the stages kb0 .. kb0 + kChunk - 1. Neighbouring threads read
+  // neighbouring bytes of a row's exponents, four at a time if rows are whole
+  // dwords (a byte per row and load, for 128 rows, cost 1.7 us a tile). Row t
+  // of the tile is row t % (16 FM) of wavefront row t / (16 FM); what lies past
+  // K's end is another row's or 0, and not used.
   const __amdgpu_buffer_rsrc_t er = buffer_rsrc(p.exps + m0 * KB, (uint32_t)mrows * (uint32_t)KB);
-  const uint32_t eoff = (uint32_t)tid * (uint32_t)KB;
-  const int eslot = (tid / (16 * FM)) * (16 * FM) + (tid & 15) * FM + (tid % (16 * FM)) / 16;
-  auto exponent = [&](int kb) {
-    return buffer_ld1(er, eoff, (uint32_t)kb);
+  const int nblks = (p.N + kLinB - 1) / kLinB;
+  auto scales = [&](int kb0) {
+    const auto put = [&](int row, int kb, uint32_t e) {
+      ex[kb * TM + (row / (16 * FM)) * (16 * FM) + (row & 15) * FM + (row % (16 * FM)) / 16] =
+          (uint8_t)e;
+    };
+    if (KB % 4 == 0) {
+      constexpr int kPer = kChunk / 4, kN = TM * kPer / S::kThreads;
+      static_assert(kN * S::kThreads == TM * kPer, "exponent loads");
+      uint32_t e[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int c = tid + S::kThreads * i;
+        e[i] = buffer_ld4(er, (uint32_t)(c / kPer) * (uint32_t)KB + kb0 + 4 * (c % kPer));
+      }
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const int c = tid + S::kThreads * i;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put(c / kPer, 4 * (c % kPer) + j, e[i] >> (8 * j));
+      }
+    } else {
+#pragma unroll 4
+      for (int c = tid; c < TM * kChunk; c += S::kThreads)
+        put(c / kChunk, c % kChunk,
+            buffer_ld1(er, (uint32_t)(c / kChunk) * (uint32_t)KB + kb0 + c % kChunk));
+    }
+    for (int i = tid; i < S::kBlocks * kChunk; i += S::kThreads) {
+      const int blk = n0 / kLinB + i / kChunk, kb = kb0 + i % kChunk;
+      sc[i] = block_scale<BF16>(
+          p.ws[(size_t)(blk < nblks ? blk : nblks - 1) * KB + (kb < KB ? kb : KB - 1)]);
+    }
   };
-  const int nblk = (n0 + wn * 16 * FN) / kLinB, nblks = (p.N + kLinB - 1) / kLinB;
-  const float* sp = p.ws + (size_t)(nblk < nblks ? nblk : nblks - 1) * KB;
 
   f32x4 acc[FN][FM];
 #pragma unroll
@@ -391,25 +444,27 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
     return operand(*reinterpret_cast<const uint4*>(row + c0),
                    *reinterpret_cast<const uint4*>(row + c1));
   };
-  auto compute = [&](const uint8_t* buf, const uint8_t* ex, float s) {
+  auto compute = [&](int kb) {
+    const uint8_t* buf = ring + (kb % NST) * S::kStage;
+    const uint8_t* e = ex + (kb % kChunk) * TM + wm * 16 * FM + l16 * FM;
+    const float s = sc[(wn * 16 * FN / kLinB) * kChunk + kb % kChunk];
     uint32_t ew[(FM + 3) / 4];
     if constexpr (FM >= 4) {
 #pragma unroll
-      for (int j = 0; j < FM / 4; ++j)
-        ew[j] = *reinterpret_cast<const uint32_t*>(ex + wm * 16 * FM + l16 * FM + 4 * j);
+      for (int j = 0; j < FM / 4; ++j) ew[j] = *reinterpret_cast<const uint32_t*>(e + 4 * j);
     } else {
       ew[0] = 0;
 #pragma unroll
-      for (int j = 0; j < FM; ++j) ew[0] |= (uint32_t)ex[wm * 16 * FM + l16 * FM + j] << (8 * j);
+      for (int j = 0; j < FM; ++j) ew[0] |= (uint32_t)e[j] << (8 * j);
     }
     i32x8_t w[FN];
 #pragma unroll
     for (int n = 0; n < FN; ++n) w[n] = fragment(buf + wbyte + n * 16 * kLinB);
     // Row tile m's products start as tile m - 1's are scaled and added: the
-    // additions of d[n] stand before the product that overwrites it, four
-    // products after the one they wait for. The barriers and pin() keep
-    // the compiler to this order (it would add a product right after its
-    // start, and gather fragments it has no registers for).
+    // additions of d[n] stand before the product that overwrites it, FN
+    // products after the one they wait for. The barriers and pin() keep the
+    // compiler to this order (it would add a product right after its start,
+    // and gather fragments it has no registers for).
     i32x8_t a = fragment(buf + abyte);
     f32x4 d[FN];
 #pragma unroll
@@ -423,41 +478,37 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
           add_block<BF16>(acc[n][m - 1], d[n], (int)ew[(m - 1) / 4], (m - 1) & 3, s);
         }
         d[n] = block_product_sel<BF16>(w[n], a, (int)ew[m / 4], m & 3);
+        __builtin_amdgcn_sched_barrier(0);
       }
       a = next;
-      __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int n = 0; n < FN; ++n)
       add_block<BF16>(acc[n][FM - 1], d[n], (int)ew[(FM - 1) / 4], (FM - 1) & 3, s);
   };
-  constexpr int kWaitVm0 = 0x0F70;  // s_waitcnt vmcnt(0)
-  float s = sp[0];
-  // one stage: start the next one's loads (past the end: the last one's
-  // again, not used), multiply, then let them be seen
-  auto stage = [&](const uint8_t* cur, const uint8_t* ecur, uint8_t* nxt, uint8_t* enxt, int kb) {
-    const int k1 = kb + 1 < KB ? kb + 1 : KB - 1;
-    const uint8_t e = exponent(k1);
-    const float s1 = sp[k1];
-    issue(nxt, k1);
-    __builtin_amdgcn_sched_barrier(0);
-    compute(cur, ecur, block_scale<BF16>(s));
-    s = s1;
-    enxt[eslot] = e;
-    __builtin_amdgcn_s_waitcnt(kWaitVm0);
-    __syncthreads();
-  };
-  issue(buf0, 0);
-  ex0[eslot] = exponent(0);
-  __builtin_amdgcn_s_waitcnt(kWaitVm0);
-  __syncthreads();
-  int kb = 0;
+#pragma unroll
+  for (int i = 0; i < NST - 1; ++i)
+    if (i < KB) issue(i);
 #pragma unroll 1
-  for (; kb + 1 < KB; kb += 2) {
-    stage(buf0, ex0, buf1, ex1, kb);
-    stage(buf1, ex1, buf0, ex0, kb + 1);
+  for (int kb = 0; kb < KB; ++kb) {
+    if (kb % kChunk == 0) {
+      if (kb > 0) lds_barrier();  // the last chunk's scales have been read
+      scales(kb);
+    }
+    // this stage's loads have ended once only those of the stages after it,
+    // NST - 2 at most, are in flight
+    const int later = KB - 1 - kb < NST - 2 ? KB - 1 - kb : NST - 2;
+    if (later <= 0)
+      wait_loads<0>();
+    else if (later == 1)
+      wait_loads<S::kLoads>();
+    else
+      wait_loads<2 * S::kLoads>();
+    // every wavefront's part is there, and the buffer read last is free
+    lds_barrier();
+    if (kb + NST - 1 < KB) issue(kb + NST - 1);
+    compute(kb);
   }
-  if (kb < KB) compute(buf0, ex0, block_scale<BF16>(s));
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
     const int64_t row = m0 + wm * 16 * FM + 16 * m + l16;
@@ -468,18 +519,18 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
   }
 }
 
-template <int TM, int TN, int WM, int WN, bool BF16>
+template <int TM, int TN, int WM, int WN, int NST, bool BF16>
 __global__ __launch_bounds__(64 * WM * WN) void linear_tile(LinearArgs p, int tiles_m,
                                                            int tiles_n) {
-  linear_tile_body<TM, TN, WM, WN, BF16>(p, tiles_m, tiles_n);
+  linear_tile_body<TM, TN, WM, WN, NST, BF16>(p, tiles_m, tiles_n);
 }
 
 static size_t al256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int TM, int TN, int WM, int WN, bool BF16>
+template <int TM, int TN, int WM, int WN, int NST, bool BF16>
 static void launch_tile(const LinearArgs& p, hipStream_t s) {
   const int tm = (int)((p.M + TM - 1) / TM), tn = (p.N + TN - 1) / TN;
-  linear_tile<TM, TN, WM, WN, BF16><<<(unsigned)((int64_t)tm * tn), 64 * WM * WN, 0, s>>>(p, tm, tn);
+  linear_tile<TM, TN, WM, WN, NST, BF16><<<(unsigned)((int64_t)tm * tn), 64 * WM * WN, 0, s>>>(p, tm, tn);
 }
 
 template <int FM, int FN, int W, int U, bool XQ, bool BF16>
@@ -503,8 +554,8 @@ static void launch_form(const LinearArgs& p, hipStream_t s) {
   if (p.M <= 64) return launch_rows<4, 1, 8, 2, false, BF16>(p, s);
   if (p.M <= 128 && tiles(128, 128) < 128) return launch_rows<8, 1, 8, 1, false, BF16>(p, s);
   if constexpr (BF16)
-    if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, BF16>(p, s);
-  launch_tile<128, 128, 2, 2, BF16>(p, s);
+    if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, BF16>(p, s);
+  launch_tile<128, 128, 2, 2, 2, BF16>(p, s);
 }
 
 static hipError_t launch_linear(const LinearArgs& p, bool bf16, hipStream_t s) {
