@@ -42,6 +42,7 @@ struct LinearArgs {
   int64_t M, ld_out;
   int N, K;
   bool vec4;  // four values of out from a feature that is a multiple of 4 are aligned
+  bool vec8;  // likewise eight bf16 values, to 16 bytes
 };
 
 __device__ __forceinline__ i32x8_t operand(uint4 a, uint4 b) {
@@ -509,6 +510,43 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
     if (kb + NST - 1 < KB) issue(kb + NST - 1);
     compute(kb);
   }
+  // bf16 rows of whole 16-byte pieces go out through LDS (the ring is free):
+  // a lane's four features of a row are half a piece, and lines of the output
+  // written in one go spare the memory system the merging (8192 x 8192 x 4096:
+  // KEPT us).
+  if constexpr (BF16 && 16 * FN * 2 == 128) {
+    if (p.vec8 && n0 + TN <= p.N) {
+      static_assert(FM * 16 * 128 * WM * WN <= NST * S::kStage, "the output tile fits the ring");
+      lds_barrier();
+      uint8_t* mine = ring + wave * (FM * 16 * 128);
+      const int col = n0 + wn * 16 * FN;
+#pragma unroll
+      for (int n = 0; n < FN; ++n) {
+        f32x4 b = {0.f, 0.f, 0.f, 0.f};
+        if (p.bias) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[j] = p.bias[col + 16 * n + 4 * q + j];
+        }
+#pragma unroll
+        for (int m = 0; m < FM; ++m) {
+          const f32x4 v = acc[n][m] + b;
+          const int piece = (2 * n + (q >> 1)) ^ (l16 & 7);
+          *reinterpret_cast<uint2*>(mine + (16 * m + l16) * 128 + 16 * piece + 8 * (q & 1)) =
+              make_uint2(f32_to_bf16_bits(v[0]) | f32_to_bf16_bits(v[1]) << 16,
+                         f32_to_bf16_bits(v[2]) | f32_to_bf16_bits(v[3]) << 16);
+        }
+      }
+      const int64_t row0 = m0 + wm * 16 * FM;
+      uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + row0 * p.ld_out + col;
+#pragma unroll
+      for (int i = 0; i < 2 * FM; ++i) {
+        const int r = 8 * i + (lane >> 3), c = lane & 7;
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + r * 128 + 16 * (c ^ (r & 7)));
+        if (row0 + r < p.M) *reinterpret_cast<uint4*>(out + (int64_t)r * p.ld_out + 8 * c) = v;
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
     const int64_t row = m0 + wm * 16 * FM + 16 * m + l16;
@@ -601,6 +639,7 @@ static moe_status linear_call(LinearArgs p, moe_dtype out_dtype, void* workspace
   }
   const size_t quad = out_dtype == MOE_BF16 ? 8 : 16;
   p.vec4 = reinterpret_cast<uintptr_t>(p.out) % quad == 0 && p.ld_out % 4 == 0;
+  p.vec8 = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.ld_out % 8 == 0;
   return launch_linear(p, out_dtype == MOE_BF16, s) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
