@@ -513,7 +513,7 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
   // bf16 rows of whole 16-byte pieces go out through LDS (the ring is free):
   // a lane's four features of a row are half a piece, and lines of the output
   // written in one go spare the memory system the merging (8192 x 8192 x 4096:
-  // KEPT us).
+  // 253 to 240 us).
   if constexpr (BF16 && 16 * FN * 2 == 128) {
     if (p.vec8 && n0 + TN <= p.N) {
       static_assert(FM * 16 * 128 * WM * WN <= NST * S::kStage, "the output tile fits the ring");
@@ -581,19 +581,65 @@ static void launch_rows(const LinearArgs& p, hipStream_t s) {
 // Whether the product quantises bf16 rows itself (one launch).
 static bool quantises_inside(int64_t M) { return M <= 16; }
 
+// Which kernel a product runs on. Times in us on one MI355X for K = 4096 (they
+// go with K), weights not in any cache.
+//
+// Up to 16 rows: the stream, 32 features a workgroup where that leaves a
+// workgroup for every compute unit, else 16 (16 x 8192: 10.2 against 14.2;
+// 16 x 4096: 10.2 against 8.7). Up to 32 rows likewise (24 x 4096: 16 features
+// 9.1, 32 features 10.6, tiles 15.6). Above, the stream of 32 x 32 while one
+// round of workgroups covers it and K gives each wavefront two blocks or more
+// (77 x 2112: 11.4, tiles 14.6; 77 x 4096, a round and a half: 19.1, tiles 15.5).
+//
+// Tiles: the kind whose rounds of workgroups cost least. A round, with as many
+// workgroups as fit the chip at once:
+//   bf16 output   256 x 256   256 workgroups  62     128 x 256   256  39
+//                 128 x 128   512 (two a compute unit)  41, or 256 with a
+//                             deeper ring  26          64 x 64    512  16
+//   fp32 output   128 x 256   256  69     128 x 128   256  41     64 x 64   256  22
+// (2048 x 4096: 56 / 39 / 41 / 49 / 63; 1000 x 4096: 54 / 34 / 32 / 26 / 33;
+// 200 x 4096: 52 / 33 / 31 / 23 / 16; 8192 x 8192: 240 / 283 / 292 / 367 / 432.)
 template <bool BF16>
 static void launch_form(const LinearArgs& p, hipStream_t s) {
-  if (p.M <= 16) return p.x ? launch_rows<1, 1, 8, 2, true, BF16>(p, s)
-                            : launch_rows<1, 1, 8, 4, false, BF16>(p, s);
-  const auto tiles = [&](int tm, int tn) {
+  const auto blocks = [&](int tm, int tn) {
     return ((p.M + tm - 1) / tm) * (int64_t)((p.N + tn - 1) / tn);
   };
-  if (p.M <= 32) return launch_rows<2, 1, 8, 2, false, BF16>(p, s);
-  if (p.M <= 64) return launch_rows<4, 1, 8, 2, false, BF16>(p, s);
-  if (p.M <= 128 && tiles(128, 128) < 128) return launch_rows<8, 1, 8, 1, false, BF16>(p, s);
-  if constexpr (BF16)
-    if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, BF16>(p, s);
-  launch_tile<128, 128, 2, 2, 2, BF16>(p, s);
+  if (p.M <= 16) {
+    const bool wide = blocks(16, 32) >= 256;
+    if (p.x)
+      return wide ? launch_rows<1, 2, 16, 1, true, BF16>(p, s)
+                  : launch_rows<1, 1, 8, 2, true, BF16>(p, s);
+    return wide ? launch_rows<1, 2, 8, 4, false, BF16>(p, s)
+                : launch_rows<1, 1, 8, 2, false, BF16>(p, s);
+  }
+  if (p.M <= 32)
+    return blocks(32, 32) >= 256 ? launch_rows<2, 2, 16, 2, false, BF16>(p, s)
+                                 : launch_rows<2, 1, 8, 2, false, BF16>(p, s);
+  if (blocks(32, 32) <= 256 && p.K >= 16 * kLinB)
+    return launch_rows<2, 2, 16, 2, false, BF16>(p, s);
+  const auto cost = [&](int tm, int tn, int round, int us) {
+    return (blocks(tm, tn) + round - 1) / round * us;
+  };
+  if constexpr (BF16) {
+    const int64_t t[] = {cost(64, 64, 512, 16), cost(128, 128, 256, 26), cost(128, 128, 512, 41),
+                         cost(128, 256, 256, 39), cost(256, 256, 256, 62)};
+    int best = 0;
+    for (int i = 1; i < 5; ++i)
+      if (t[i] < t[best]) best = i;
+    switch (best) {
+      case 0: return launch_tile<64, 64, 4, 1, 3, BF16>(p, s);
+      case 1: return launch_tile<128, 128, 4, 2, 4, BF16>(p, s);
+      case 2: return launch_tile<128, 128, 4, 2, 2, BF16>(p, s);
+      case 3: return launch_tile<128, 256, 2, 4, 3, BF16>(p, s);
+      default: return launch_tile<256, 256, 2, 4, 2, BF16>(p, s);
+    }
+  } else {
+    const int64_t t0 = cost(64, 64, 256, 22), t1 = cost(128, 128, 256, 41),
+                  t2 = cost(128, 256, 256, 69);
+    if (t0 <= t1 && t0 <= t2) return launch_tile<64, 64, 2, 2, 4, BF16>(p, s);
+    if (t1 <= t2) return launch_tile<128, 128, 4, 2, 2, BF16>(p, s);
+    launch_tile<128, 256, 2, 4, 3, BF16>(p, s);
+  }
 }
 
 static hipError_t launch_linear(const LinearArgs& p, bool bf16, hipStream_t s) {
