@@ -8,6 +8,7 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -482,22 +483,23 @@ _DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _UNREAD = 256  # address given for an empty tensor, whose memory no call touches
 
 
-def _place(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> torch.device:
-    dev = first.device
-    for t in rest:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors must be on one GPU")
-    if dev.type != "cuda":
+def _place(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> int:
+    """The GPU that all these tensors are on."""
+    index = first.get_device()
+    if index < 0:
         raise ValueError("tensors must be on one GPU")
-    return dev
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            raise ValueError("tensors must be on one GPU")
+    return index
 
 
 def _rows(t: torch.Tensor, what: str) -> int:
     """Distance in elements between the rows of a 2-D tensor with unit column
     stride (columns broadcast or out of order are refused)."""
     if t.dim() == 2:
-        ld, step = t.stride()
         rows, cols = t.shape
+        ld, step = t.stride()
         if step == 1 or cols <= 1:
             return ld if rows > 1 else cols
     raise ValueError(f"{what} must be 2-D with contiguous rows")
@@ -512,26 +514,31 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else (t.data_ptr() or _UNREAD)
 
 
-def _empty(shape, dtype, dev, stream):
-    if stream is None:  # the device's current stream
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _empty(like: torch.Tensor, shape, dtype, stream):
+    """On like's GPU, for use on `stream` (None: the GPU's current stream)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _enqueue(name: str, dev: torch.device, stream, *args):
-    """Calls the C function on the tensors' device and the given or that
-    device's current stream. (The raw handle is what current_stream() wraps;
-    building the wrapper takes as long as the rest of a small call's checks.)"""
-    fn = getattr(_lib or load(), name)
-    index = dev.index
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+def _enqueue(fn, name: str, index: int, stream, *args):
+    """Calls the C function `fn` on GPU `index` and the given stream or that
+    GPU's current one. (The raw handles are what torch.cuda.current_stream() and
+    current_device() wrap; the wrappers take as long as the rest of a small
+    call's checks.)"""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device_index == index:
+        s = stream.cuda_stream
+    else:
+        raise ValueError("stream must be on the tensors' GPU")
+    if index == torch._C._cuda_getDevice():
         st = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             st = fn(*args, s)
-    if st != MOE_OK:
+    if st:
         raise MoeError(st, name)
 
 
@@ -557,14 +564,17 @@ def moe_select_experts(logits: torch.Tensor, top_k: int, gating: Gating,
     (topk_idx [T][k] int32, gates [T][k] fp32)."""
     dev = _place(logits, balance_bias)
     ld = _rows(logits, "logits")
-    T, E = logits.shape
-    if logits.dtype not in _DTYPES:
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
         raise ValueError("logits must be float32 or bfloat16")
+    T, E = logits.shape
     _flat(balance_bias, (E,), torch.float32, "balance_bias")
-    idx = _empty((T, max(top_k, 0)), torch.int32, dev, stream)
-    gates = _empty((T, max(top_k, 0)), torch.float32, dev, stream)
-    _enqueue("moe_select_experts", dev, stream, _addr(logits), _DTYPES[logits.dtype], ld,
-             _addr(balance_bias), gating.ref, T, E, top_k, _addr(idx), _addr(gates))
+    k = max(top_k, 0)
+    idx = _empty(logits, (T, k), torch.int32, stream)
+    gates = _empty(logits, (T, k), torch.float32, stream)
+    _enqueue((_lib or load()).moe_select_experts, "moe_select_experts", dev, stream,
+             _addr(logits), dtype, ld, _addr(balance_bias), gating.ref, T, E, top_k, _addr(idx),
+             _addr(gates))
     return idx, gates
 
 
@@ -581,14 +591,15 @@ def moe_route_gated(x: torch.Tensor, router_w: torch.Tensor, top_k: int, gating:
     _flat(router_bias, (E,), torch.float32, "router_bias")
     _flat(balance_bias, (E,), torch.float32, "balance_bias")
     cfg = make_config(T, H, E, inter, top_k, block, False, x.dtype, torch.float32)
-    idx = _empty((T, max(top_k, 0)), torch.int32, dev, stream)
-    gates = _empty((T, max(top_k, 0)), torch.float32, dev, stream)
-    logits = _empty((T, E), torch.float32, dev, stream) if with_logits else None
+    k = max(top_k, 0)
+    idx = _empty(x, (T, k), torch.int32, stream)
+    gates = _empty(x, (T, k), torch.float32, stream)
+    logits = _empty(x, (T, E), torch.float32, stream) if with_logits else None
     if workspace is None:
-        workspace = _empty(max(1, workspace_bytes(cfg)), torch.uint8, dev, stream)
-    _enqueue("moe_route_gated", dev, stream, _addr(x), _addr(router_w), _addr(router_bias),
-             _addr(balance_bias), gating.ref, _addr(idx), _addr(gates), _addr(logits),
-             ctypes.byref(cfg), _addr(workspace), workspace.numel())
+        workspace = _empty(x, (max(1, workspace_bytes(cfg)),), torch.uint8, stream)
+    _enqueue(load().moe_route_gated, "moe_route_gated", dev, stream, _addr(x), _addr(router_w),
+             _addr(router_bias), _addr(balance_bias), gating.ref, _addr(idx), _addr(gates),
+             _addr(logits), ctypes.byref(cfg), _addr(workspace), _bytes(workspace))
     return (idx, gates, logits) if with_logits else (idx, gates)
 
 
@@ -599,7 +610,8 @@ def moe_forward_gated(x: torch.Tensor, router_w: torch.Tensor, bank: Bank, top_k
                       path: str = "auto", out: Optional[torch.Tensor] = None,
                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The whole layer with the gated choice of experts, through moe_forward_gated."""
-    dev = _place(x, router_w, router_bias, balance_bias, bank.w_gate_up, out, workspace)
+    dev = _place(x, router_w, router_bias, balance_bias, bank.w_gate_up, out, workspace,
+                 None if shared is None else shared.w_gate_up)
     _dev(x)
     T, H = x.shape
     E = router_w.shape[0]
@@ -613,42 +625,54 @@ def moe_forward_gated(x: torch.Tensor, router_w: torch.Tensor, bank: Bank, top_k
     if shared is not None:
         shared.check(1, H, I, block)
     if out is None:
-        out = _empty((T, H), out_dtype, dev, stream)
+        out = _empty(x, (T, H), out_dtype, stream)
     if workspace is None:
-        workspace = _empty(max(1, workspace_bytes(cfg)), torch.uint8, dev, stream)
-    _enqueue("moe_forward_gated", dev, stream, _addr(x), _addr(router_w), _addr(router_bias),
-             _addr(balance_bias), gating.ref, ctypes.byref(bank.c),
-             ctypes.byref(shared.c) if shared is not None else None, top_k, _addr(out),
-             ctypes.byref(cfg), _addr(workspace), workspace.numel(), None)
+        workspace = _empty(x, (max(1, workspace_bytes(cfg)),), torch.uint8, stream)
+    _enqueue(load().moe_forward_gated, "moe_forward_gated", dev, stream, _addr(x),
+             _addr(router_w), _addr(router_bias), _addr(balance_bias), gating.ref,
+             ctypes.byref(bank.c), ctypes.byref(shared.c) if shared is not None else None, top_k,
+             _addr(out), ctypes.byref(cfg), _addr(workspace), _bytes(workspace), None)
     return out
 
 
+def _bytes(t: Optional[torch.Tensor]) -> int:
+    if t is None:
+        return 0
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
+@functools.lru_cache(maxsize=1024)
 def linear_workspace_bytes(rows: int, out_features: int, in_features: int, x_is_codes: bool) -> int:
+    """moe_linear_workspace_bytes (a function of the sizes alone)."""
     return int(load().moe_linear_workspace_bytes(rows, out_features, in_features,
                                                  int(bool(x_is_codes))))
 
 
-def _linear(name, dev, stream, head, codes, w, w_scales, bias, M, K, out_dtype, out, workspace):
+def _linear(name, dev, stream, like, a0, a1, codes, w, w_scales, bias, M, K, out_dtype, out,
+            workspace):
     N = w.shape[0]
     _flat(w, (N, K), torch.uint8, "w")
     _flat(w_scales, (-(-N // 128), K // 128), torch.float32, "w_scales")
     _flat(bias, (N,), torch.float32, "bias")
     if out is None:
-        if out_dtype not in _DTYPES:
+        code = _DTYPES.get(out_dtype)
+        if code is None:
             raise ValueError(f"unsupported dtype {out_dtype}")
-        out = _empty((M, N), out_dtype, dev, stream)
+        out = _empty(like, (M, N), out_dtype, stream)
         ld_out = N
     else:
-        if out.dtype not in _DTYPES or tuple(out.shape) != (M, N):
+        code = _DTYPES.get(out.dtype)
+        if code is None or out.shape != (M, N):
             raise ValueError(f"out must be a float32 or bfloat16 tensor of shape {(M, N)}")
         ld_out = _rows(out, "out")
-        out_dtype = out.dtype
-    ws_bytes = load().moe_linear_workspace_bytes(M, N, K, codes)
-    if workspace is None and ws_bytes:
-        workspace = _empty(ws_bytes, torch.uint8, dev, stream)
-    _enqueue(name, dev, stream, *head, _addr(w), _addr(w_scales), _addr(bias), M, N, K, _addr(out),
-             ld_out, _DTYPES[out_dtype], _addr(workspace),
-             0 if workspace is None else workspace.numel() * workspace.element_size())
+    if workspace is None:
+        need = linear_workspace_bytes(M, N, K, codes)
+        if need:
+            workspace = _empty(like, (need,), torch.uint8, stream)
+    _enqueue(getattr(_lib or load(), name), name, dev, stream, a0, a1, _addr(w), _addr(w_scales),
+             _addr(bias), M, N, K, _addr(out), ld_out, code, _addr(workspace), _bytes(workspace))
     return out
 
 
@@ -664,7 +688,7 @@ def moe_linear(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
     if x.dtype != torch.bfloat16:
         raise ValueError("x must be bfloat16")
     M, K = x.shape
-    return _linear("moe_linear", dev, stream, (_addr(x), ld), 0, w, w_scales, bias, M, K,
+    return _linear("moe_linear", dev, stream, x, _addr(x), ld, False, w, w_scales, bias, M, K,
                    out_dtype, out, workspace)
 
 
@@ -681,8 +705,8 @@ def moe_linear_e4m3(codes: torch.Tensor, exps: torch.Tensor, w: torch.Tensor,
     M, K = codes.shape
     _flat(codes, (M, K), torch.uint8, "codes")
     _flat(exps, (M, K // 128), torch.uint8, "exps")
-    return _linear("moe_linear_e4m3", dev, stream, (_addr(codes), _addr(exps)), 1, w, w_scales,
-                   bias, M, K, out_dtype, out, workspace)
+    return _linear("moe_linear_e4m3", dev, stream, codes, _addr(codes), _addr(exps), True, w,
+                   w_scales, bias, M, K, out_dtype, out, workspace)
 
 
 def moe_swiglu_quantize_e4m3(gate_up: torch.Tensor, stream=None):
@@ -690,11 +714,12 @@ def moe_swiglu_quantize_e4m3(gate_up: torch.Tensor, stream=None):
     (E4M3 codes [T][I] uint8, E8M0 exponents [T][I/128] uint8)."""
     dev = _place(gate_up)
     ld = _rows(gate_up, "gate_up")
-    if gate_up.dtype != torch.bfloat16 or gate_up.shape[1] % 2:
+    T, two = gate_up.shape
+    if gate_up.dtype != torch.bfloat16 or two % 2:
         raise ValueError("gate_up must be bfloat16 with an even number of columns")
-    T, I = gate_up.shape[0], gate_up.shape[1] // 2
-    codes = _empty((T, I), torch.uint8, dev, stream)
-    exps = _empty((T, I // 128), torch.uint8, dev, stream)
-    _enqueue("moe_swiglu_quantize_e4m3", dev, stream, _addr(gate_up), ld, T, I, _addr(codes),
-             _addr(exps))
+    I = two // 2
+    codes = _empty(gate_up, (T, I), torch.uint8, stream)
+    exps = _empty(gate_up, (T, I // 128), torch.uint8, stream)
+    _enqueue((_lib or load()).moe_swiglu_quantize_e4m3, "moe_swiglu_quantize_e4m3", dev, stream,
+             _addr(gate_up), ld, T, I, _addr(codes), _addr(exps))
     return codes, exps
