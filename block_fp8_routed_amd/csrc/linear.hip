@@ -392,8 +392,8 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
       load_to_lds(at + TM * kLinB + 16 * S::kThreads * i, off0 + i * step, wr, k);
   };
   // Scales of the stages kb0 .. kb0 + kChunk - 1. Neighbouring threads read
-  // neighbouring bytes of a row's exponents, four at a time if rows are whole
-  // dwords (a byte per row and load, for 128 rows, cost 1.7 us a tile). Row t
+  // neighbouring bytes of a row's exponents, four at a time if rows are whole,
+  // aligned dwords (a byte per row and load, for 128 rows, cost 1.7 us a tile). Row t
   // of the tile is row t % (16 FM) of wavefront row t / (16 FM); what lies past
   // K's end is another row's or 0, and not used.
   const __amdgpu_buffer_rsrc_t er = buffer_rsrc(p.exps + m0 * KB, (uint32_t)mrows * (uint32_t)KB);
@@ -403,7 +403,7 @@ __device__ __forceinline__ void linear_tile_body(const LinearArgs& p, int tiles_
       ex[kb * TM + (row / (16 * FM)) * (16 * FM) + (row & 15) * FM + (row % (16 * FM)) / 16] =
           (uint8_t)e;
     };
-    if (KB % 4 == 0) {
+    if (KB % 4 == 0 && reinterpret_cast<uintptr_t>(p.exps) % 4 == 0) {
       constexpr int kPer = kChunk / 4, kN = TM * kPer / S::kThreads;
       static_assert(kN * S::kThreads == TM * kPer, "exponent loads");
       uint32_t e[kN];
@@ -655,7 +655,9 @@ static moe_status check_sizes(int64_t M, int32_t N, int32_t K) {
   if (K % kLinB != 0) return MOE_ERR_UNSUPPORTED;
   // 32-bit offsets within a tile, the tiles' count, and the quantiser's grid
   if (K > (1 << 22) || N > (1 << 24) || M > (1 << 20) ||
-      (M + 15) / 16 * ((N + 63) / 64) >= ((int64_t)1 << 31) || M * (K / kLinB) >= ((int64_t)1 << 27)) return MOE_ERR_UNSUPPORTED;
+      (M + 15) / 16 * ((N + 63) / 64) >= ((int64_t)1 << 31) ||
+      M * (K / kLinB) >= ((int64_t)1 << 27))
+    return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

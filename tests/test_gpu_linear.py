@@ -168,6 +168,27 @@ def test_activation_range(M):
     run(M, 160, K, x=x, scales=s)
 
 
+@pytest.mark.parametrize("M", [5, 70, 300])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_exponents_at_any_address(M, out_dtype):
+    """Exponents that start at an odd byte; out that starts at an odd element."""
+    import block_fp8_routed_amd as moe
+    N, K = 200, 1024
+    x = rows(M, K, M)
+    w, s = (torch.from_numpy(a).cuda() for a in weights(N, K, M))
+    codes, exps = moe.moe_quantize_act_e4m3(x.cuda())
+    want = moe.moe_linear_e4m3(codes, exps, w, s, out_dtype=out_dtype)
+    for skip in (1, 2, 3):
+        buf = torch.empty(exps.numel() + 4, dtype=torch.uint8, device="cuda")
+        moved = buf[skip:skip + exps.numel()].view(exps.shape)
+        moved.copy_(exps)
+        flat = torch.zeros(M * N + 4, dtype=out_dtype, device="cuda")
+        out = flat[skip:skip + M * N].view(M, N)
+        moe.moe_linear_e4m3(codes, moved, w, s, out=out)
+        assert torch.equal(out, want), skip
+        assert not flat[:skip].any() and not flat[skip + M * N:].any(), skip
+
+
 def test_a_row_does_not_depend_on_the_others():
     """Each row of a batch has the bits it has in another batch of the same
     size, whatever the other rows hold."""
