@@ -23,10 +23,11 @@
 // group and is chosen only when the kept groups run out of others (then the
 // lowest index first, gate 0).
 //
-// One wavefront per token. Lane L owns nv consecutive experts L nv, L nv + 1,
+// A token takes LPT lanes. Lane L of it owns nv consecutive experts L nv, L nv + 1,
 // ...: the lowest lane that holds a value then holds the lowest expert with
 // it, and where nv divides the group size a lane lies in one group.
 #include <cmath>
+#include <type_traits>
 
 #include "gate_select.hpp"
 #include "layer.hpp"
@@ -149,15 +150,84 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[N]) {
           }
 }
 
-// LDS of one wavefront. Expert i of lane L is at L NV + i.
-template <int NV>
+// ---- values across the LPT lanes (16 or 64) of a token ----
+// Four DPP steps leave a 16-lane row's total in all its lanes; rows and halves
+// of the wavefront then meet in gfx950's lane swaps: with both operands the
+// same register, one result holds the even rows (the lower half) twice and the
+// other the odd ones.
+template <int LPT, class Op>
+__device__ __forceinline__ uint32_t token_reduce(uint32_t v, Op op) {
+  v = op(v, (uint32_t)dpp_i<kDppXor1>((int)v));
+  v = op(v, (uint32_t)dpp_i<kDppXor2>((int)v));
+  v = op(v, (uint32_t)dpp_i<kDppHalfMirror>((int)v));
+  v = op(v, (uint32_t)dpp_i<kDppMirror>((int)v));
+  if (LPT == 64) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op((uint32_t)r[0], (uint32_t)r[1]);
+    const auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op((uint32_t)h[0], (uint32_t)h[1]);
+  }
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+  return token_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v) {
+  return __uint_as_float(token_reduce<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+__device__ __forceinline__ double make_f64(uint32_t lo, uint32_t hi) {
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+template <int LPT>
+__device__ __forceinline__ double token_sum(double v) {
+  const auto step = [&](auto ctrl) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    v += make_f64((uint32_t)dpp_i<decltype(ctrl)::value>((int)(uint32_t)b),
+                  (uint32_t)dpp_i<decltype(ctrl)::value>((int)(b >> 32)));
+  };
+  step(std::integral_constant<int, kDppXor1>());
+  step(std::integral_constant<int, kDppXor2>());
+  step(std::integral_constant<int, kDppHalfMirror>());
+  step(std::integral_constant<int, kDppMirror>());
+  if (LPT == 64) {
+    uint64_t b = (uint64_t)__double_as_longlong(v);
+    auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false);
+    auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false,
+                                               false);
+    v = make_f64(lo[0], hi[0]) + make_f64(lo[1], hi[1]);
+    b = (uint64_t)__double_as_longlong(v);
+    lo = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false);
+    hi = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+    v = make_f64(lo[0], hi[0]) + make_f64(lo[1], hi[1]);
+  }
+  return v;
+}
+// the token's bits of a wavefront mask, at bit 0
+template <int LPT>
+__device__ __forceinline__ uint64_t token_bits(unsigned long long b, int base) {
+  if (LPT == 64) return b;
+  const uint32_t half = base & 32 ? (uint32_t)(b >> 32) : (uint32_t)b;
+  return (half >> (base & 16)) & 0xffffu;
+}
+template <int LPT>
+__device__ __forceinline__ int first_bit(uint64_t b) {
+  return LPT == 64 ? __ffsll((unsigned long long)b) - 1 : __ffs((uint32_t)b) - 1;
+}
+
+// LDS of one wavefront. Expert i of lane L is at slot L NV + i.
+template <int NV, int LPT>
 struct GateLds {
   float raw[64 * NV];     // logits, -inf for masked and absent experts
-  uint64_t key[64 * NV];  // choose_exact: order keys of c
-  union {
-    uint32_t head[2][64];  // each lane's two largest keys; the ranked choice
-    double pair[2][64];    // exact_groups: each lane's two largest c
-  };
+  uint64_t key[LPT * NV]; // exact choice of one token: order keys of c, by expert
+  uint32_t head[2][64];   // each lane's two largest keys
+  alignas(16) float gs[64];  // groups' scores
+  float2 edge[2][4];      // the last group kept and the first dropped: score, magnitude
+  uint2 list[64];         // lane j of a token: the j-th key drawn and its slot
+  double c[64];           // c of the drawn experts
 };
 
 // The wavefront's own LDS traffic is in order; this keeps the compiler to it.
@@ -166,19 +236,13 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-// The softmax's sum of e^(l - top) over the lane's NV logits and the wavefront.
-template <int NV>
-__device__ __forceinline__ double softmax_sum(const float* raw, float top) {
+// The softmax's sum of e^(l - top) over the token's lanes, nv logits each.
+template <int LPT>
+__device__ __forceinline__ double softmax_sum(int nv, const float* raw, float top) {
   double z = 0.0;
 #pragma unroll 2
-  for (int i = 0; i < NV; ++i) z += exp64((double)raw[i] - (double)top);  // (-inf adds 0)
-  return wave_sum_f64(z);
+  for (int i = 0; i < nv; ++i) z += exp64((double)raw[i] - (double)top);  // (-inf adds 0)
+  return token_sum<LPT>(z);
 }
 
 // An expert's score from its logit (-inf: masked); softmax: not yet divided
@@ -190,129 +254,101 @@ __device__ __forceinline__ double score64(const GateRule& r, float logit, float 
   return logit > kMaskedLogit ? s : 0.0;
 }
 
-// The groups that come first by their scores in lanes 0 .. groups - 1 (keys),
-// as a mask.
-__device__ __forceinline__ unsigned long long first_groups(const GateRule& r, uint64_t key) {
+// ---- the exact choice, one token by the whole wavefront ----
+// Rolled loops over LDS (few tokens come here). base: the token's first lane;
+// lanes take every 64th expert.
+
+// keys of c of all experts into lds.key
+template <int NV, int LPT>
+__device__ __forceinline__ void exact_keys(const GateRule& r, int base, float top,
+                                           const float* __restrict__ balance, GateLds<NV, LPT>& lds) {
   const int lane = threadIdx.x & 63;
+  double z = 1.0;
+  if (r.softmax) {
+    z = 0.0;
+    for (int e = lane; e < r.experts; e += 64)
+      z += exp64((double)lds.raw[(base + e / r.nv) * NV + e % r.nv] - (double)top);
+    z = token_sum<64>(z);
+  }
+#pragma unroll 1
+  for (int e = lane; e < r.experts; e += 64) {
+    const float v = lds.raw[(base + e / r.nv) * NV + e % r.nv];
+    double c = score64(r, v, top);
+    if (r.softmax) c = z > 0.0 ? c / z : 0.0;
+    if (balance) c += (double)balance[e];
+    lds.key[e] = v > kMaskedLogit ? order_key(c) : kKeyMasked;
+  }
+  wave_lds_fence();
+}
+
+// the kept groups by lds.key, as a mask
+template <int NV, int LPT>
+__device__ __forceinline__ unsigned long long exact_groups(const GateRule& r, GateLds<NV, LPT>& lds) {
+  const int lane = threadIdx.x & 63;
+  uint64_t mine = 0;  // lane g: the key of group g's score
+#pragma unroll 1
+  for (int g = 0; g < r.groups; ++g) {
+    uint64_t a = 0, b = 0;  // the group's two largest keys among the lane's experts
+    for (int j = lane; j < r.per_group; j += 64) {
+      const uint64_t c = lds.key[g * r.per_group + j];
+      if (c > a) {
+        b = a;
+        a = c;
+      } else if (c > b) {
+        b = c;
+      }
+    }
+    const uint64_t m = wave_max_u64(a);
+    const int wl = __ffsll((unsigned long long)__ballot(a == m)) - 1;
+    const uint64_t m2 = wave_max_u64(lane == wl ? b : a);
+    uint64_t k = kKeyMasked;
+    if (m > kKeyMasked)
+      k = order_key(key_value(m) + (r.rank > 1 && m2 > kKeyMasked ? key_value(m2) : 0.0));
+    if (lane == g) mine = k;
+  }
   int before = 0;
   for (int j = 0; j < r.groups; ++j) {
-    const uint64_t o = readlane_u64(key, j);
-    before += o > key || (o == key && j < lane) ? 1 : 0;
+    const uint64_t o = readlane_u64(mine, j);
+    before += o > mine || (o == mine && j < lane) ? 1 : 0;
   }
   return __ballot(lane < r.groups && before < r.top_groups);
 }
 
-// The choice by fp64 keys, for any group size: lane j < top_k gets the j-th
-// (as a slot of GateLds). Rolled loops over LDS: it runs for few tokens.
-template <int NV>
-__device__ __forceinline__ int choose_exact(const GateRule& r, float top,
-                                            const float* __restrict__ balance, GateLds<NV>& lds) {
-  const int lane = threadIdx.x & 63, e0 = lane * r.nv;
-  const float* raw = lds.raw + lane * NV;
-  uint64_t* key = lds.key + lane * NV;
-  const double z = r.softmax ? softmax_sum<NV>(raw, top) : 1.0;
-#pragma unroll 1
-  for (int i = 0; i < r.nv; ++i) {
-    const int e = e0 + i;
-    const float v = raw[i];
-    double c = score64(r, v, top);
-    if (r.softmax) c = z > 0.0 ? c / z : 0.0;
-    if (balance && e < r.experts) c += (double)balance[e];
-    key[i] = e < r.experts ? (v > kMaskedLogit ? order_key(c) : kKeyMasked) : kKeyAbsent;
-  }
-  wave_lds_fence();
+// the whole choice: slots into lds.list[base + j].y, j < top_k
+template <int NV, int LPT>
+__device__ __forceinline__ void choose_exact(const GateRule& r, int base, float top,
+                                             const float* __restrict__ balance,
+                                             GateLds<NV, LPT>& lds) {
+  const int lane = threadIdx.x & 63;
+  exact_keys<NV, LPT>(r, base, top, balance, lds);
   if (r.groups > 1) {
-    double gs = -INFINITY;  // lane g: group g's score
-    for (int g = 0; g < r.groups; ++g) {
-      // the group's two largest keys, lanes taking every 64th expert
-      uint64_t a = 0, b = 0;
-      for (int j = lane; j < r.per_group; j += 64) {
-        const int e = g * r.per_group + j, l = e / r.nv;
-        const uint64_t c = lds.key[l * NV + e - l * r.nv];
-        if (c > a) {
-          b = a;
-          a = c;
-        } else if (c > b) {
-          b = c;
-        }
-      }
-      const uint64_t m = wave_max_u64(a);
-      const int wl = __ffsll((unsigned long long)__ballot(a == m)) - 1;
-      const uint64_t m2 = wave_max_u64(lane == wl ? b : a);
-      double s = m > kKeyMasked ? key_value(m) : -INFINITY;
-      if (r.rank > 1 && m2 > kKeyMasked) s += key_value(m2);
-      if (lane == g) gs = s;
-    }
-    const unsigned long long kept = first_groups(r, gs > -INFINITY ? order_key(gs) : kKeyMasked);
+    const unsigned long long kept = exact_groups<NV, LPT>(r, lds);
+    wave_lds_fence();
 #pragma unroll 1
-    for (int i = 0; i < r.nv; ++i)
-      if (e0 + i < r.experts && !((kept >> ((e0 + i) / r.per_group)) & 1)) key[i] = kKeyAbsent;
+    for (int e = lane; e < r.experts; e += 64)
+      if (!((kept >> (e / r.per_group)) & 1)) lds.key[e] = kKeyAbsent;
+    wave_lds_fence();
   }
-  uint64_t best = 0;  // the lane's largest key and its lowest place
-  int place = 0;
-  const auto rescan = [&] {
-    best = 0;
 #pragma unroll 1
-    for (int i = 0; i < r.nv; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        place = i;
-      }
-  };
-  rescan();
-  int mine = 0;
   for (int j = 0; j < r.top_k; ++j) {
+    uint64_t best = 0;
+    int at = 0;
+    for (int e = lane; e < r.experts; e += 64) {
+      const uint64_t c = lds.key[e];
+      if (c > best) {
+        best = c;
+        at = e;
+      }
+    }
     const uint64_t m = wave_max_u64(best);
-    const int wl = __ffsll((unsigned long long)__ballot(best == m)) - 1;
-    const int slot = wl * NV + __builtin_amdgcn_readlane(place, wl);
-    if (lane == j) mine = slot;
-    if (lane == wl) {
-      key[place] = kKeyAbsent;
-      rescan();
+    // the lowest expert that holds it (largest complement)
+    const int e = (int)~wave_max_u32(best == m ? ~(uint32_t)at : 0u);
+    if (lane == 0) {
+      lds.list[base + j].y = (uint32_t)((base + e / r.nv) * NV + e % r.nv);
+      lds.key[e] = kKeyAbsent;
     }
+    wave_lds_fence();
   }
-  return mine;
-}
-
-// The kept groups by fp64 scores, as a mask of groups, where every lane lies
-// in one group.
-template <int NV>
-__device__ __forceinline__ unsigned long long exact_groups(const GateRule& r, float top,
-                                                           const float* __restrict__ balance,
-                                                           GateLds<NV>& lds) {
-  const int lane = threadIdx.x & 63, e0 = lane * r.nv;
-  const float* raw = lds.raw + lane * NV;
-  const double z = r.softmax ? softmax_sum<NV>(raw, top) : 1.0;
-  double a = -INFINITY, b = -INFINITY;
-#pragma unroll 1
-  for (int i = 0; i < r.nv; ++i) {
-    double c = score64(r, raw[i], top) / z;
-    if (balance && e0 + i < r.experts) c += (double)balance[e0 + i];
-    if (!(raw[i] > kMaskedLogit)) c = -INFINITY;
-    b = fmax(b, fmin(a, c));
-    a = fmax(a, c);
-  }
-  wave_lds_fence();
-  lds.pair[0][lane] = a;
-  lds.pair[1][lane] = b;
-  wave_lds_fence();
-  a = b = -INFINITY;
-  if (lane < r.groups)
-    for (int j = 0; j < r.group_lanes; ++j) {
-      const double c = lds.pair[0][lane * r.group_lanes + j];
-      b = fmax(fmax(b, fmin(a, c)), lds.pair[1][lane * r.group_lanes + j]);
-      a = fmax(a, c);
-    }
-  const double gs = r.rank > 1 && b > -INFINITY ? a + b : a;
-  wave_lds_fence();
-  return first_groups(r, a > -INFINITY ? order_key(gs) : kKeyMasked);
-}
-
-__device__ __forceinline__ bool uniform_bool(bool b) { return __ballot(b) != 0ull; }
-
-// A uniform value that the compiler takes for one per lane.
-__device__ __forceinline__ float uniform(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, v)));
 }
 
 // fp32 values as unsigned keys in the same order (no NaN).
@@ -324,10 +360,9 @@ __device__ __forceinline__ float value32(uint32_t h) {
   return __uint_as_float(h ^ ((uint32_t)((int32_t)~h >> 31) | 0x80000000u));
 }
 
-// The choice by fp32 keys, made exact where they are close. False: not
-// possible this way (masked experts have to be chosen, or more than
-// kCandidates are too close to tell). Lane j < top_k gets the j-th expert (as
-// a slot of GateLds).
+// The choice by fp32 keys, made exact where they are close; slots into
+// lds.list[base + j].y, j < top_k. False for a token where that is not possible
+// (masked experts have to be chosen, or too many are too close to tell).
 //   Without a bias, and where a group's score is its best expert's, the
 // logits' own order is the order of c: keys are the logits. Two count as close
 // if they differ by 2^-40 or less, or lie where the score hardly moves any more
@@ -338,18 +373,18 @@ __device__ __forceinline__ float value32(uint32_t h) {
 // bounds what the rounded l - top does).
 //   A key's low bits hold the expert's place in its lane, so that a lane's keys
 // can be sorted as plain numbers; what they displace (cut) counts as error too.
-//   The wavefront draws the largest key top_k times, and on while the next one
-// is close to the last of these. If any two neighbours are close, the drawn
-// ones (one per lane) are ranked by fp64 c and index.
-constexpr int kCandidates = 32;
-template <int NV, bool BF16>
+//   A token draws its largest key top_k times, and on while the next one is
+// close to the last of these. If any two neighbours are close, the drawn ones
+// (one per lane) are ranked by fp64 c and index.
+template <int NV, int LPT, bool BF16>
 __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[NV], float top,
                                             const float (&bias)[NV],
-                                            const float* __restrict__ balance, GateLds<NV>& lds,
-                                            int& mine) {
+                                            const float* __restrict__ balance,
+                                            GateLds<NV, LPT>& lds) {
   constexpr int kLow = NV <= 1 ? 0 : NV <= 2 ? 1 : NV <= 4 ? 2 : NV <= 8 ? 3 : 4;
   constexpr uint32_t kPlace = (1u << kLow) - 1u;
-  const int lane = threadIdx.x & 63;
+  constexpr int kCandidates = LPT < 32 ? LPT : 32;
+  const int lane = threadIdx.x & 63, tl = lane & (LPT - 1), base = lane - tl;
   const bool by_logit = !balance && (r.groups == 1 || r.rank == 1);
   uint32_t key[NV];
   float eps = 0.f;
@@ -364,11 +399,11 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
       c[i] = __expf(v[i] - top);  // 0 for masked experts
       z += c[i];
     }
-    z = uniform(group_sum<64>(z));
+    z = token_sum<LPT>(z);
     const float q = z > 0.f ? 1.0f / z : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) c[i] = fmaf(c[i], q, bias[i]);
-    eps = uniform(0x1p-18f * q + 0x1p-22f);
+    eps = 0x1p-18f * q + 0x1p-22f;
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -392,13 +427,14 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
     lds.head[0][lane] = key[0] >> kLow;
     if constexpr (NV > 1) lds.head[1][lane] = key[1] >> kLow;
     wave_lds_fence();
+    // lane g of the token: group g
     const int lg = r.group_lanes;
     uint32_t a = 0, b = 0;
     for (int j0 = 0; j0 < lg; j0 += 8) {  // eight lanes' keys requested together
       uint32_t x[8], y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int at = lane * lg + j0 + j;
+        const int at = base + tl * lg + j0 + j;
         x[j] = lds.head[0][at < 64 ? at : 63];
         if constexpr (NV > 1) y[j] = lds.head[1][at < 64 ? at : 63];
       }
@@ -410,100 +446,125 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
         if constexpr (NV > 1) b = max(b, j0 + j < lg ? y[j] : 0u);
       }
     }
-    const bool in = lane < r.groups, two = r.rank > 1 && b != 0u;
+    const bool in = tl < r.groups, two = r.rank > 1 && b != 0u;
     const float av = value32(a << kLow), bv = two ? value32(b << kLow) : 0.f;
     const float gs = in && a != 0u ? av + bv : -INFINITY;
     const float mag = a != 0u ? fabsf(av) + fabsf(bv) : 0.f;
+    lds.gs[lane] = gs;
+    wave_lds_fence();
     int before = 0;
-    for (int j = 0; j < r.groups; ++j) {
-      const float o = readlane_f(gs, j);
-      before += o > gs || (o == gs && j < lane) ? 1 : 0;
+    for (int j0 = 0; j0 < r.groups; j0 += 4) {  // (lanes past the groups hold -inf)
+      const float4 o = *reinterpret_cast<const float4*>(&lds.gs[base + j0]);
+      before += o.x > gs || (o.x == gs && j0 < tl) ? 1 : 0;
+      before += o.y > gs || (o.y == gs && j0 + 1 < tl) ? 1 : 0;
+      before += o.z > gs || (o.z == gs && j0 + 2 < tl) ? 1 : 0;
+      before += o.w > gs || (o.w == gs && j0 + 3 < tl) ? 1 : 0;
     }
-    unsigned long long kept = __ballot(in && before < r.top_groups);
+    uint64_t kept = token_bits<LPT>(__ballot(in && before < r.top_groups), base);
     if (r.top_groups < r.groups) {
-      // the last group kept and the first one dropped
-      const int lk = __ffsll(__ballot(in && before == r.top_groups - 1)) - 1;
-      const int ld = __ffsll(__ballot(in && before == r.top_groups)) - 1;
-      const float sk = readlane_f(gs, lk), sd = readlane_f(gs, ld);
-      const float m = fmaxf(readlane_f(mag, lk), readlane_f(mag, ld));
+      if (in && before == r.top_groups - 1) lds.edge[0][base / 16] = make_float2(gs, mag);
+      if (in && before == r.top_groups) lds.edge[1][base / 16] = make_float2(gs, mag);
+      wave_lds_fence();
+      const float2 k = lds.edge[0][base / 16], d = lds.edge[1][base / 16];
       // (a bf16 logit loses nothing to its place's bits: equal keys are equal scores)
-      const bool sure = by_logit ? sk > -INFINITY && (!close(sk, sd) || (BF16 && sk == sd))
-                                 : sk - sd > 4.0f * eps + 4.0f * kCut * m;
-      if (!sure) kept = exact_groups(r, top, balance, lds);
+      const bool sure = by_logit ? k.x > -INFINITY && (!close(k.x, d.x) || (BF16 && k.x == d.x))
+                                 : k.x - d.x > 4.0f * eps + 4.0f * kCut * fmaxf(k.y, d.y);
+      unsigned long long todo = __ballot(!sure);
+      while (todo) {
+        const int at = (__ffsll(todo) - 1) & ~(LPT - 1);
+        exact_keys<NV, LPT>(r, at, readlane_f(top, at), balance, lds);
+        const unsigned long long exact = exact_groups<NV, LPT>(r, lds);
+        if (base == at) kept = exact;
+        todo &= LPT == 64 ? 0ull : ~(((1ull << (LPT & 63)) - 1ull) << at);
+        wave_lds_fence();
+      }
     }
-    const int own = (int)(((float)lane + 0.5f) * r.inv_group_lanes);
+    const int own = (int)(((float)tl + 0.5f) * r.inv_group_lanes);
     const bool mykept = own < r.groups && ((kept >> own) & 1);
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = mykept ? key[i] : 0u;
   }
-  uint32_t got = 0, m = 0;  // lane j: the j-th key; the last one drawn
-  mine = 0;
-  // draws the largest key m (found before) as the n-th
-  const auto draw = [&](uint32_t h, int n) {
-    const int wl = __ffsll((unsigned long long)__ballot(h == m)) - 1;
-    const int wi = (int)(kPlace - ((uint32_t)__builtin_amdgcn_readlane((int)key[0], wl) & kPlace));
-    got = lane == n ? m : got;
-    mine = lane == n ? wl * NV + wi : mine;
-    const bool pop = lane == wl;
+  // the lane that holds the token's largest key m first draws it as the n-th
+  const auto draw = [&](uint32_t h, uint32_t m, int n, bool on) {
+    const int wl = first_bit<LPT>(token_bits<LPT>(__ballot(h == m), base));
+    if (on && tl == wl) {
+      lds.list[base + n] = make_uint2(m, (uint32_t)(lane * NV) + (kPlace - (key[0] & kPlace)));
 #pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = pop ? (i + 1 < NV ? key[i + 1] : 0u) : key[i];
+      for (int i = 0; i + 1 < NV; ++i) key[i] = key[i + 1];
+      key[NV - 1] = 0u;
+    }
   };
+  uint32_t m = 0;
   for (int j = 0; j < r.top_k; ++j) {
     const uint32_t h = key[0] >> kLow;
-    m = wave_max_u32(h);
-    draw(h, j);
+    m = token_max<LPT>(h);
+    draw(h, m, j, true);
   }
-  if (m == 0u) return false;
+  bool ok = m != 0u;
   const float last = value32(m << kLow);
   int n = r.top_k;
-  for (;; ++n) {
+  for (;;) {
     const uint32_t h = key[0] >> kLow;
-    m = wave_max_u32(h);
-    if (m == 0u || !uniform_bool(close(last, value32(m << kLow)))) break;
-    if (n == kCandidates) return false;
-    draw(h, n);
+    m = token_max<LPT>(h);
+    bool more = ok && m != 0u && close(last, value32(m << kLow));
+    if (more && n == kCandidates) ok = more = false;
+    if (!__ballot(more)) break;
+    draw(h, m, n, more);
+    n += more ? 1 : 0;
   }
+  wave_lds_fence();
   // neighbours: far enough apart, or the same numbers (the lower index came first)
-  const float x = value32(got << kLow), y = __shfl_down(x, 1);
-  const float lj = lds.raw[mine], ln = __shfl_down(lj, 1);
-  const bool unsure = lane + 1 < n && close(x, y) && (balance || lj != ln);
-  if (n > r.top_k || __ballot(unsure)) {
-    const int l = mine / NV, e = l * r.nv + mine - l * NV;
-    double cx = score64(r, lj, top);
+  const uint2 won = lds.list[lane], next = lds.list[lane < 63 ? lane + 1 : 63];
+  const bool mine = ok && tl < n;
+  const float lj = lds.raw[mine ? won.y : 0];
+  const float ln = lds.raw[ok && tl + 1 < n ? next.y : 0];
+  const bool unsure = ok && tl + 1 < n && close(value32(won.x << kLow), value32(next.x << kLow)) &&
+                      (balance || lj != ln);
+  const bool rank = ok && (n > r.top_k || token_bits<LPT>(__ballot(unsure), base) != 0);
+  if (__ballot(rank)) {
+    const int slot = mine ? (int)won.y - base * NV : 0, l = slot / NV;
+    const int e = l * r.nv + slot - l * NV;
+    double cx = mine ? score64(r, lj, top) : 0.0;
     if (balance) {
-      if (r.softmax) cx /= softmax_sum<NV>(lds.raw + lane * NV, top);
+      if (r.softmax) cx /= softmax_sum<LPT>(r.nv, lds.raw + lane * NV, top);
       cx += (double)balance[e];
     }
-    const uint64_t ck = order_key(cx);
+    lds.c[lane] = cx;
+    lds.head[0][lane] = (uint32_t)e;
+    wave_lds_fence();
     int before = 0;
-    for (int j = 0; j < n; ++j) {
-      const uint64_t o = readlane_u64(ck, j);
-      const int oe = __builtin_amdgcn_readlane(e, j);
-      before += o > ck || (o == ck && oe < e) ? 1 : 0;
+    for (int j = 0; __ballot(rank && j < n); ++j) {
+      const double o = lds.c[base + j];
+      const int oe = (int)lds.head[0][base + j];
+      before += j < n && (o > cx || (o == cx && oe < e)) ? 1 : 0;
     }
     wave_lds_fence();
-    if (lane < n) lds.head[0][before] = (uint32_t)mine;
+    if (rank && mine) lds.list[base + before].y = won.y;
     wave_lds_fence();
-    mine = lane < r.top_k ? (int)lds.head[0][lane] : 0;
   }
-  return true;
+  return ok;
 }
 
-template <int NV, class Logits, bool BALANCE>
+// LPT lanes per token: 64, or 16 where tokens fill the chip (launch).
+template <int NV, int LPT, class Logits, bool BALANCE>
 __global__ __launch_bounds__(256) void gate_select_kernel(Logits lg,
                                                          const float* __restrict__ balance_,
                                                          GateRule r, int64_t T,
                                                          int32_t* __restrict__ topk,
                                                          float* __restrict__ gates,
                                                          int32_t* __restrict__ zero_word) {
-  __shared__ GateLds<NV> all[4];
+  __shared__ GateLds<NV, LPT> all[4];
   if (zero_word && blockIdx.x == 0 && threadIdx.x == 0) *zero_word = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  if (t >= T) return;  // (no workgroup barrier follows)
-  GateLds<NV>& lds = all[wave];
+  const int tl = lane & (LPT - 1), base = lane - tl;
+  const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * (64 / LPT);
+  if (t0 >= T) return;  // (no workgroup barrier follows)
+  // a token past the end repeats the last one and stores nothing
+  const int64_t t = t0 + base / LPT < T ? t0 + base / LPT : T - 1;
+  const bool there = t0 + base / LPT < T;
+  GateLds<NV, LPT>& lds = all[wave];
   const float* balance = BALANCE ? balance_ : nullptr;
-  const int e0 = lane * r.nv;
+  const int e0 = tl * r.nv;
   float v[NV], bias[NV];
   lg.template load<NV>(v, t, r, e0);
 #pragma unroll
@@ -518,52 +579,82 @@ __global__ __launch_bounds__(256) void gate_select_kernel(Logits lg,
     top = fmaxf(top, v[i]);
     lds.raw[lane * NV + i] = v[i];
   }
-  // (a token without any expert left: 0, so that no difference is NaN)
-  if (r.softmax) top = fmaxf(wave_max_f32(top), -3.402823466e38f);
-  top = uniform(top);
+  // (a token without any expert left: not -inf, so that no difference is NaN)
+  if (r.softmax) top = fmaxf(value32(token_max<LPT>(order32(top))), -3.402823466e38f);
   wave_lds_fence();
-  int mine = 0;
-  if (!(r.fast && choose_fast<NV, Logits::kBf16>(r, v, top, bias, balance, lds, mine)))
-    mine = choose_exact<NV>(r, top, balance, lds);
+  const bool ok = r.fast && choose_fast<NV, LPT, Logits::kBf16>(r, v, top, bias, balance, lds);
+  for (unsigned long long todo = __ballot(!ok); todo;) {
+    const int at = (__ffsll(todo) - 1) & ~(LPT - 1);
+    choose_exact<NV, LPT>(r, at, readlane_f(top, at), balance, lds);
+    todo &= LPT == 64 ? 0ull : ~(((1ull << (LPT & 63)) - 1ull) << at);
+  }
   // gates
-  double s = lane < r.top_k ? score64(r, lds.raw[mine], top) : 0.0;
+  const bool mine = tl < r.top_k;
+  const int slot = mine ? (int)lds.list[lane].y : base * NV;
+  double s = mine ? score64(r, lds.raw[slot], top) : 0.0;
   double den = 1.0;
-  if (r.renorm) {
-    den = s;
-#pragma unroll
-    for (int o = 8; o; o >>= 1) den += __shfl_xor(den, o, 16);
-  } else if (r.softmax) {
-    den = softmax_sum<NV>(lds.raw + lane * NV, top);
+  if (r.renorm)
+    den = token_sum<16>(s);  // (top_k <= 16)
+  else if (r.softmax)
+    den = softmax_sum<LPT>(r.nv, lds.raw + lane * NV, top);
+  if (mine && there) {
+    const int l = (slot - base * NV) / NV;
+    topk[t * r.top_k + tl] = l * r.nv + slot - base * NV - l * NV;
+    gates[t * r.top_k + tl] = (float)(den > 0.0 ? s / den * (double)r.scale : 0.0);
   }
-  if (lane < r.top_k) {
-    const int l = mine / NV;
-    topk[t * r.top_k + lane] = l * r.nv + mine - l * NV;
-    gates[t * r.top_k + lane] = (float)(den > 0.0 ? s / den * (double)r.scale : 0.0);
-  }
+}
+
+// Experts per lane where LPT lanes take a token: the fewest that cover all;
+// with groups, of those that divide a group, if there is one up to 16 (else 0).
+static int lane_experts(const GateRule& r, int lpt) {
+  int nv = (r.experts + lpt - 1) / lpt;
+  if (r.groups > 1)
+    while (nv <= 16 && r.per_group % nv != 0) ++nv;
+  return nv <= 16 && (r.groups == 1 || r.groups <= lpt) ? nv : 0;
 }
 
 template <class Logits>
 static hipError_t launch(const Logits& lg, const float* balance, GateRule r, int64_t T,
-                         int32_t* topk, float* gates, int32_t* zero_word, bool vec, hipStream_t s) {
-  const dim3 grid((unsigned)((T + 3) / 4));
+                         int32_t* topk, float* gates, int32_t* zero_word, int align,
+                         hipStream_t s) {
+  // Four tokens share a wavefront, and its instructions, where there are enough
+  // of them to fill the chip; before that a token's own way through is what
+  // counts. Measured, 64 lanes a token against 16, us: bf16 softmax, 128
+  // experts, top 8: 2048 tokens 6.0 / 6.6, 4096 7.1 / 6.6, 8192 9.7 / 7.2, 30001
+  // 23.7 / 13.8; 160 experts in 8 groups, top 6: 4096 8.5 / 8.8, 30001 33.1 /
+  // 23.4. Two tokens of 512 experts: 16384 38.2 / 39.2, so not there.
+  const bool share = T >= 4096 && r.experts <= 256 && lane_experts(r, 16) != 0;
+  const int lpt = share ? 16 : 64;
+  r.nv = lane_experts(r, lpt);
+  r.fast = r.nv != 0;
+  if (!r.fast) r.nv = (r.experts + 63) / 64;
+  r.group_lanes = r.per_group / r.nv;
+  r.inv_group_lanes = 1.0f / (float)(r.group_lanes ? r.group_lanes : 1);
   const int nv = r.nv;
-  const int full = nv <= 1 ? 1 : nv <= 2 ? 2 : nv <= 4 ? 4 : nv <= 8 ? 8 : 16;
-  r.vec = vec && nv == full && r.experts % nv == 0;
-#define MOE_GATE(NV)                                                                          \
-  balance ? gate_select_kernel<NV, Logits, true><<<grid, 256, 0, s>>>(lg, balance, r, T, topk, \
-                                                                      gates, zero_word)       \
-          : gate_select_kernel<NV, Logits, false><<<grid, 256, 0, s>>>(lg, nullptr, r, T, topk, \
-                                                                       gates, zero_word)
-  if (nv <= 1)
-    MOE_GATE(1);
-  else if (nv <= 2)
-    MOE_GATE(2);
-  else if (nv <= 4)
-    MOE_GATE(4);
-  else if (nv <= 8)
-    MOE_GATE(8);
-  else
-    MOE_GATE(16);
+  const dim3 grid((unsigned)((T + 256 / lpt - 1) / (256 / lpt)));
+  const int full = nv <= 1 && lpt == 64   ? 1
+                   : nv <= 2 && lpt == 64 ? 2
+                   : nv <= 4              ? 4
+                   : nv <= 8              ? 8
+                                          : 16;
+  // vector loads: whole lanes, on the boundary that their reach asks for
+  const int size = Logits::kBf16 ? 2 : 4, span = nv * size < 16 ? nv * size : 16;
+  r.vec = nv == full && r.experts % nv == 0 && align % span == 0;
+#define MOE_GATE(NV, LPT)                                                                     \
+  balance ? gate_select_kernel<NV, LPT, Logits, true><<<grid, 256, 0, s>>>(                   \
+                lg, balance, r, T, topk, gates, zero_word)                                    \
+          : gate_select_kernel<NV, LPT, Logits, false><<<grid, 256, 0, s>>>(                  \
+                lg, nullptr, r, T, topk, gates, zero_word)
+  switch (100 * lpt + full) {
+    case 6401: MOE_GATE(1, 64); break;
+    case 6402: MOE_GATE(2, 64); break;
+    case 6404: MOE_GATE(4, 64); break;
+    case 6408: MOE_GATE(8, 64); break;
+    case 6416: MOE_GATE(16, 64); break;
+    case 1604: MOE_GATE(4, 16); break;
+    case 1608: MOE_GATE(8, 16); break;
+    default: MOE_GATE(16, 16);
+  }
 #undef MOE_GATE
   return hipGetLastError();
 }
@@ -586,20 +677,6 @@ moe_status gate_rule(const moe_gating* g, int experts, int top_k, GateRule* r) {
   r->per_group = per;
   r->top_groups = g->top_groups;
   r->rank = g->group_rank;
-  r->lanes_per_group = 1;
-  while (2 * r->lanes_per_group * g->groups <= 64) r->lanes_per_group *= 2;
-  // experts per lane: the fewest that cover all; with groups, of those that
-  // divide a group, if there is one up to 16
-  const int least = (experts + 63) / 64;
-  r->nv = least;
-  r->fast = true;
-  if (g->groups > 1) {
-    while (r->nv <= 16 && per % r->nv != 0) ++r->nv;
-    r->fast = r->nv <= 16;
-    if (!r->fast) r->nv = least;
-  }
-  r->group_lanes = r->fast ? per / r->nv : 0;
-  r->inv_group_lanes = r->fast ? 1.0f / (float)r->group_lanes : 0.f;
   r->softmax = g->score == MOE_SCORE_SOFTMAX;
   r->renorm = g->renormalise;
   r->scale = g->scale;
@@ -611,7 +688,7 @@ hipError_t launch_gate_select(const Dims& d, const GateRule& r, const float* plo
                               float* gates, float* logits_out, int32_t* zero_word,
                               hipStream_t s) {
   return launch(SliceLogits{plog, router_slices(d), d.T, router_bias, logits_out}, balance, r, d.T,
-                topk, gates, zero_word, false, s);
+                topk, gates, zero_word, 1, s);
 }
 
 }  // namespace moe
@@ -632,15 +709,15 @@ extern "C" moe_status moe_select_experts(const void* logits, moe_dtype dtype, in
   if (!logits || !topk_idx || !gates) return MOE_ERR_NULL;
   if (tokens == 0) return MOE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // vector loads of a lane's experts: rows and the first of each lane 16-byte
-  // aligned, or as far as a lane's experts reach
-  const int64_t size = dtype == MOE_BF16 ? 2 : 4, span = r.nv * size < 16 ? r.nv * size : 16;
-  const bool vec = reinterpret_cast<uintptr_t>(logits) % span == 0 && ld * size % span == 0;
+  // the largest power of two, up to 16, that every row's address is a multiple of
+  const int64_t size = dtype == MOE_BF16 ? 2 : 4;
+  int align = 16;
+  while (reinterpret_cast<uintptr_t>(logits) % align != 0 || ld * size % align != 0) align /= 2;
   const hipError_t e =
       dtype == MOE_BF16
           ? launch(MatrixLogits<true>{logits, ld}, balance_bias, r, tokens, topk_idx, gates,
-                   nullptr, vec, s)
+                   nullptr, align, s)
           : launch(MatrixLogits<false>{logits, ld}, balance_bias, r, tokens, topk_idx, gates,
-                   nullptr, vec, s);
+                   nullptr, align, s);
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

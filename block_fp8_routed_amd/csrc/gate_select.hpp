@@ -13,7 +13,6 @@ constexpr float kMaskedLogit = -3.3e38f;  // at or below: the expert is masked
 struct GateRule {
   int experts, top_k;
   int groups, per_group, top_groups, rank;
-  int lanes_per_group;  // largest power of two with lanes_per_group * groups <= 64
   int nv;               // experts per lane, consecutive ones
   bool vec;             // a lane's logits can be read with vector loads
   bool fast;            // every lane lies in one group: fp32 keys first

@@ -148,6 +148,39 @@ def test_long_batch():
           group_rank=1, renormalise=False, scale=16.0)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,k,groups,top,rank", [
+    (1, 1, 1, 1, 1), (7, 7, 1, 1, 1), (40, 3, 1, 1, 1), (64, 16, 16, 5, 2), (100, 6, 4, 2, 2),
+    (128, 8, 1, 1, 1), (160, 6, 8, 3, 1), (200, 16, 1, 1, 1), (256, 8, 8, 4, 2), (255, 9, 15, 4, 2),
+    (256, 16, 32, 5, 2), (257, 8, 1, 1, 1)])
+def test_many_tokens(E, k, groups, top, rank, score, dtype):
+    """Batches long enough that tokens share a wavefront, the last one part
+    full, with and without a bias."""
+    l = draw(4099, E, E + k, dtype=dtype)
+    rule = dict(score=score, groups=groups, top_groups=top, group_rank=rank, scale=1.5)
+    check(l, k, bias(E, k, 0.05), ld_pad=5, **rule)
+    check(l, k, None, renormalise=False, **rule)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_masks_and_ties_among_many_tokens(score):
+    """Tokens of one wavefront that need different ways: masked to a few
+    experts or none, equal scores, and ordinary ones."""
+    E, k = 128, 9
+    rng = np.random.default_rng(8)
+    l = draw(4500, E, 3)
+    l[::7] = torch.from_numpy(rng.integers(0, 3, (len(l[::7]), E)).astype(np.float32))
+    l[::11, 4:] = float("-inf")
+    l[::13] = float("nan")
+    l[1::17, :64] = torch.finfo(torch.float32).min
+    l[2::19, 5] = float("inf")
+    for groups in (1, 16):
+        rule = dict(score=score, groups=groups, top_groups=max(1, groups // 3), group_rank=2)
+        check(l, k, bias(E, 3, 0.5), **rule)
+        check(l, k, None, **rule)
+
+
 def test_no_tokens():
     import block_fp8_routed_amd as moe
     idx, gates = moe.moe_select_experts(torch.empty(0, 64, device="cuda"), 4, moe.Gating())
