@@ -223,7 +223,7 @@ template <int NV, int LPT>
 struct GateLds {
   float raw[64 * NV];     // logits, -inf for masked and absent experts
   uint64_t key[LPT * NV]; // exact choice of one token: order keys of c, by expert
-  uint32_t head[2][64];   // each lane's two largest keys
+  float head[2][64];      // each lane's two largest c
   alignas(16) float gs[64];  // groups' scores
   float2 edge[2][4];      // the last group kept and the first dropped: score, magnitude
   uint2 list[64];         // lane j of a token: the j-th key drawn and its slot
@@ -376,7 +376,7 @@ __device__ __forceinline__ float value32(uint32_t h) {
 //   A token draws its largest key top_k times, and on while the next one is
 // close to the last of these. If any two neighbours are close, the drawn ones
 // (one per lane) are ranked by fp64 c and index.
-template <int NV, int LPT, bool BF16>
+template <int NV, int LPT>
 __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[NV], float top,
                                             const float (&bias)[NV],
                                             const float* __restrict__ balance,
@@ -424,14 +424,22 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
     return !(x - y > 2.0f * eps + kCut * fmaxf(fabsf(x), fabsf(y)));
   };
   if (r.groups > 1) {
-    lds.head[0][lane] = key[0] >> kLow;
-    if constexpr (NV > 1) lds.head[1][lane] = key[1] >> kLow;
+    // (from c itself: the keys' cut would leave a group's score eight times less sure)
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const float x = v[i] > kMaskedLogit ? c[i] : -INFINITY;
+      b = fmaxf(b, fminf(a, x));
+      a = fmaxf(a, x);
+    }
+    lds.head[0][lane] = a;
+    if constexpr (NV > 1) lds.head[1][lane] = b;
     wave_lds_fence();
     // lane g of the token: group g
     const int lg = r.group_lanes;
-    uint32_t a = 0, b = 0;
-    for (int j0 = 0; j0 < lg; j0 += 8) {  // eight lanes' keys requested together
-      uint32_t x[8], y[8];
+    a = b = -INFINITY;
+    for (int j0 = 0; j0 < lg; j0 += 8) {  // eight lanes' values requested together
+      float x[8], y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int at = base + tl * lg + j0 + j;
@@ -440,16 +448,15 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j0 + j >= lg) x[j] = 0;
-        b = max(b, min(a, x[j]));
-        a = max(a, x[j]);
-        if constexpr (NV > 1) b = max(b, j0 + j < lg ? y[j] : 0u);
+        if (j0 + j >= lg) x[j] = -INFINITY;
+        b = fmaxf(b, fminf(a, x[j]));
+        a = fmaxf(a, x[j]);
+        if constexpr (NV > 1) b = fmaxf(b, j0 + j < lg ? y[j] : -INFINITY);
       }
     }
-    const bool in = tl < r.groups, two = r.rank > 1 && b != 0u;
-    const float av = value32(a << kLow), bv = two ? value32(b << kLow) : 0.f;
-    const float gs = in && a != 0u ? av + bv : -INFINITY;
-    const float mag = a != 0u ? fabsf(av) + fabsf(bv) : 0.f;
+    const bool in = tl < r.groups, two = r.rank > 1 && b > -INFINITY;
+    const float gs = in ? a + (two ? b : 0.f) : -INFINITY;
+    const float mag = (a > -INFINITY ? fabsf(a) : 0.f) + (two ? fabsf(b) : 0.f);
     lds.gs[lane] = gs;
     wave_lds_fence();
     int before = 0;
@@ -466,9 +473,10 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
       if (in && before == r.top_groups) lds.edge[1][base / 16] = make_float2(gs, mag);
       wave_lds_fence();
       const float2 k = lds.edge[0][base / 16], d = lds.edge[1][base / 16];
-      // (a bf16 logit loses nothing to its place's bits: equal keys are equal scores)
-      const bool sure = by_logit ? k.x > -INFINITY && (!close(k.x, d.x) || (BF16 && k.x == d.x))
-                                 : k.x - d.x > 4.0f * eps + 4.0f * kCut * fmaxf(k.y, d.y);
+      // (logits that are equal are equal scores; nothing is sure of two empty groups)
+      const bool sure = k.x > -INFINITY &&
+                        (by_logit ? k.x == d.x || !close(k.x, d.x)
+                                  : k.x - d.x > 4.0f * eps + 0x1p-22f * fmaxf(k.y, d.y));
       unsigned long long todo = __ballot(!sure);
       while (todo) {
         const int at = (__ffsll(todo) - 1) & ~(LPT - 1);
@@ -530,12 +538,12 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
       cx += (double)balance[e];
     }
     lds.c[lane] = cx;
-    lds.head[0][lane] = (uint32_t)e;
+    lds.list[lane].x = (uint32_t)e;
     wave_lds_fence();
     int before = 0;
     for (int j = 0; __ballot(rank && j < n); ++j) {
       const double o = lds.c[base + j];
-      const int oe = (int)lds.head[0][base + j];
+      const int oe = (int)lds.list[base + j].x;
       before += j < n && (o > cx || (o == cx && oe < e)) ? 1 : 0;
     }
     wave_lds_fence();
@@ -582,7 +590,7 @@ __global__ __launch_bounds__(256) void gate_select_kernel(Logits lg,
   // (a token without any expert left: not -inf, so that no difference is NaN)
   if (r.softmax) top = fmaxf(value32(token_max<LPT>(order32(top))), -3.402823466e38f);
   wave_lds_fence();
-  const bool ok = r.fast && choose_fast<NV, LPT, Logits::kBf16>(r, v, top, bias, balance, lds);
+  const bool ok = r.fast && choose_fast<NV, LPT>(r, v, top, bias, balance, lds);
   for (unsigned long long todo = __ballot(!ok); todo;) {
     const int at = (__ffsll(todo) - 1) & ~(LPT - 1);
     choose_exact<NV, LPT>(r, at, readlane_f(top, at), balance, lds);
