@@ -230,12 +230,6 @@ struct GateLds {
   double c[64];           // c of the drawn experts
 };
 
-// The wavefront's own LDS traffic is in order; this keeps the compiler to it.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // The softmax's sum of e^(l - top) over the token's lanes, nv logits each.
 template <int LPT>
 __device__ __forceinline__ double softmax_sum(int nv, const float* raw, float top) {

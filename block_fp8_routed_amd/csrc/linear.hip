@@ -170,12 +170,16 @@ __device__ __forceinline__ void linear_tile_of(int b, int tiles_m, int tiles_n, 
 
 // Small batches: the weights' bytes bound the product, so it is laid out as a
 // stream of them. A workgroup takes 16 FN output features and up to 16 FM
-// rows; its W wavefronts take every W-th block of K, weights and activations
-// straight from global memory into operand registers (a load instruction
-// covers 64 bytes of each of 16 weight rows), U blocks requested together; the
-// partial sums meet in LDS and are added in wavefront order. The products are
-// the exact fp16 ones for both output types: the matrix units have room to
-// spare here.
+// rows; its W wavefronts take every W-th block of K, U blocks requested
+// together; the partial sums meet in LDS and are added in wavefront order. The
+// products are the exact fp16 ones for both output types: the matrix units
+// have room to spare here.
+//   A load covers whole 128-byte lines (eight rows of codes, four of bf16). The
+// matrix instruction wants 16 rows and a quarter of the columns in each
+// wavefront's quarter instead, so a wavefront passes its blocks through LDS of
+// its own. Loads straight in that form, half lines of 16 rows, take 28 B/ns into a
+// compute unit, whatever hangs on them (77 x 2112 x 4096: 11.4 us; so 7.9; with
+// the exchange left out 7.3).
 //   XQ: the activations are bf16 rows of x, quantised as they are read: a
 // lane holds 32 of a row's 128 columns, the row's four lanes agree on the
 // largest magnitude, and the conversion instruction does the rest. Each
@@ -201,33 +205,50 @@ __device__ __forceinline__ i32x8_t quantised_operand(const uint4 (&v)[4], int& e
 
 template <int FM, int FN, int W, int U, bool XQ, bool BF16>
 __device__ __forceinline__ void linear_rows_body(const LinearArgs& p) {
-  __shared__ f32x4 red[W][FM * FN][64];
+  constexpr int AL = XQ ? 4 : 2;  // loads of a fragment of activations
+  constexpr int kWave = 1024 * (FM * AL + FN * 2);
+  static_assert(kWave >= 1024 * FM * FN, "partial sums take the blocks' place");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W * kWave];
   const int lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const mine = lds + wave * kWave;
   const int n0 = blockIdx.x * 16 * FN;
   const int64_t m0 = (int64_t)blockIdx.y * 16 * FM;
   const int KB = p.K / kLinB;
-  const uint8_t* wp[FN];
+  // load j of a fragment: rows 8 j + lane / 8, 16-byte piece lane % 8
+  const uint8_t* wp[FN][2];
   const float* sp[FN];
 #pragma unroll
   for (int n = 0; n < FN; ++n) {
     const int nt = n0 + 16 * n < p.N ? n0 + 16 * n : n0;  // a tile past the end repeats the first
-    const int r = nt + l16 < p.N ? nt + l16 : p.N - 1;
-    wp[n] = p.w + (size_t)r * p.K + 16 * q;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int r = nt + 8 * j + (lane >> 3) < p.N ? nt + 8 * j + (lane >> 3) : p.N - 1;
+      wp[n][j] = p.w + (size_t)r * p.K + 16 * (lane & 7);
+    }
     sp[n] = p.ws + (size_t)(nt / kLinB) * KB;
   }
-  const uint8_t* ap[FM];
+  // (bf16: rows 4 j + lane / 16, piece lane % 16)
+  const uint8_t* ap[FM][AL];
   const uint8_t* ep[FM];
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
-    const int64_t r = m0 + 16 * m + l16 < p.M ? m0 + 16 * m + l16 : p.M - 1;
-    if (XQ) {
-      ap[m] = reinterpret_cast<const uint8_t*>(p.x + r * p.ld_x + 16 * q);
-    } else {
-      ap[m] = p.codes + (size_t)r * p.K + 16 * q;
-      ep[m] = p.exps + (size_t)r * KB;
+    const int64_t t = m0 + 16 * m, last = p.M - 1;
+#pragma unroll
+    for (int j = 0; j < AL; ++j) {
+      const int64_t r = XQ ? t + 4 * j + q : t + 8 * j + (lane >> 3);
+      if (XQ)
+        ap[m][j] = reinterpret_cast<const uint8_t*>(p.x + (r < last ? r : last) * p.ld_x + 8 * l16);
+      else
+        ap[m][j] = p.codes + (size_t)(r < last ? r : last) * p.K + 16 * (lane & 7);
     }
+    if (!XQ) ep[m] = p.exps + (size_t)(t + l16 < last ? t + l16 : last) * KB;
   }
+  // Piece c of row r is at slot c ^ (r / 2 % 8) of the row's 128 bytes, or
+  // c ^ r % 16 of its 256: both sides of the exchange reach all banks.
+  const int r8 = lane >> 3;
+  const int put8 = 128 * r8 + 16 * ((lane & 7) ^ (r8 >> 1));   // j: + 1024 j, piece ^ 4 j
+  const int get8 = 128 * l16 + 16 * (q ^ (l16 >> 1));          // second half: piece ^ 4
   f32x4 acc[FN][FM];
 #pragma unroll
   for (int n = 0; n < FN; ++n)
@@ -236,7 +257,7 @@ __device__ __forceinline__ void linear_rows_body(const LinearArgs& p) {
 
   // U blocks a round; blocks past the end repeat the last one with scale 0
   for (int kb0 = wave; kb0 < KB; kb0 += W * U) {
-    uint4 w[U][FN][2], av[U][FM][XQ ? 4 : 2];
+    uint4 w[U][FN][2], av[U][FM][AL];
     int ev[U][FM];
     float s[U][FN];
 #pragma unroll
@@ -244,53 +265,72 @@ __device__ __forceinline__ void linear_rows_body(const LinearArgs& p) {
       const int k0 = kb0 + u * W, kb = k0 < KB ? k0 : KB - 1;
 #pragma unroll
       for (int n = 0; n < FN; ++n) {
-        w[u][n][0] = ld16(wp[n] + (size_t)kb * kLinB);
-        w[u][n][1] = ld16(wp[n] + (size_t)kb * kLinB + 64);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[u][n][j] = ld16(wp[n][j] + (size_t)kb * kLinB);
         s[u][n] = k0 < KB ? sp[n][kb] : 0.f;
       }
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
-        if (XQ) {
-          const uint8_t* x = ap[m] + (size_t)kb * (2 * kLinB);
-          av[u][m][0] = ld16(x);
-          av[u][m][1] = ld16(x + 16);
-          av[u][m][2] = ld16(x + 128);
-          av[u][m][3] = ld16(x + 144);
-        } else {
-          av[u][m][0] = ld16(ap[m] + (size_t)kb * kLinB);
-          av[u][m][1] = ld16(ap[m] + (size_t)kb * kLinB + 64);
-          ev[u][m] = ep[m][kb];
-        }
+#pragma unroll
+        for (int j = 0; j < AL; ++j)
+          av[u][m][j] = ld16(ap[m][j] + (size_t)kb * (XQ ? 2 * kLinB : kLinB));
+        if (!XQ) ev[u][m] = ep[m][kb];
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      const auto store = [&](int at, uint4 v) { *reinterpret_cast<uint4*>(mine + at) = v; };
+      const auto fetch = [&](int at) { return *reinterpret_cast<const uint4*>(mine + at); };
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) store(2048 * n + 1024 * j + (put8 ^ 64 * j), w[u][n][j]);
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
+#pragma unroll
+        for (int j = 0; j < AL; ++j)
+          store(2048 * FN + 1024 * (AL * m + j) +
+                    (XQ ? 256 * q + 16 * (l16 ^ (4 * j + q)) : put8 ^ 64 * j),
+                av[u][m][j]);
+      wave_lds_fence();
+      i32x8_t b[FN], a[FM];
+      int e[FM];
+#pragma unroll
+      for (int n = 0; n < FN; ++n)
+        b[n] = operand(fetch(2048 * n + get8), fetch(2048 * n + (get8 ^ 64)));
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
-        i32x8_t a;
-        int e;
+        const int at = 2048 * FN + 1024 * AL * m;
         if constexpr (XQ) {
-          a = quantised_operand(av[u][m], e);
+          // columns 16 q .. and 64 + 16 q ..: pieces 2 q, 2 q + 1, and those + 8
+          const int g = at + 256 * l16, c = 2 * q;
+          const uint4 v[4] = {fetch(g + 16 * (c ^ l16)), fetch(g + 16 * ((c + 1) ^ l16)),
+                              fetch(g + 16 * ((c + 8) ^ l16)), fetch(g + 16 * ((c + 9) ^ l16))};
+          a[m] = quantised_operand(v, e[m]);
         } else {
-          a = operand(av[u][m][0], av[u][m][1]);
-          e = ev[u][m];
+          a[m] = operand(fetch(at + get8), fetch(at + (get8 ^ 64)));
+          e[m] = ev[u][m];
         }
+      }
+      wave_lds_fence();
+#pragma unroll
+      for (int m = 0; m < FM; ++m)
 #pragma unroll
         for (int n = 0; n < FN; ++n)
-          add_block<false>(acc[n][m],
-                           block_product<false, 0>(operand(w[u][n][0], w[u][n][1]), a, e), e, 0,
-                           s[u][n]);
-      }
+          add_block<false>(acc[n][m], block_product<false, 0>(b[n], a[m], e[m]), e[m], 0, s[u][n]);
+    }
   }
+  f32x4* red = reinterpret_cast<f32x4*>(mine) + lane;
 #pragma unroll
   for (int n = 0; n < FN; ++n)
 #pragma unroll
-    for (int m = 0; m < FM; ++m) red[wave][n * FM + m][lane] = acc[n][m];
+    for (int m = 0; m < FM; ++m) red[(n * FM + m) * 64] = acc[n][m];
   __syncthreads();
   for (int t = wave; t < FM * FN; t += W) {
-    f32x4 v = red[0][t][lane];
+    const uint8_t* at = lds + 1024 * t + 16 * lane;
+    f32x4 v = *reinterpret_cast<const f32x4*>(at);
 #pragma unroll
-    for (int i = 1; i < W; ++i) v += red[i][t][lane];
+    for (int i = 1; i < W; ++i) v += *reinterpret_cast<const f32x4*>(at + i * kWave);
     const int64_t row = m0 + 16 * (t % FM) + l16;
     if (row < p.M) store4<BF16>(p, row, n0 + 16 * (t / FM) + 4 * q, v);
   }
@@ -584,12 +624,17 @@ static bool quantises_inside(int64_t M) { return M <= 16; }
 // Which kernel a product runs on. Times in us on one MI355X for K = 4096 (they
 // go with K), weights not in any cache.
 //
-// Up to 16 rows: the stream, 32 features a workgroup where that leaves a
-// workgroup for every compute unit, else 16 (16 x 8192: 10.2 against 14.2;
-// 16 x 4096: 10.2 against 8.7). Up to 32 rows likewise (24 x 4096: 16 features
-// 9.1, 32 features 10.6, tiles 15.6). Above, the stream of 32 x 32 while one
-// round of workgroups covers it and K gives each wavefront two blocks or more
-// (77 x 2112: 11.4, tiles 14.6; 77 x 4096, a round and a half: 19.1, tiles 15.5).
+// Up to 16 rows: the stream, 16 features a workgroup, or 32 where that would
+// ask for a second round of them (16 x 8192: 32 features 9.4, 16 features 13.2;
+// 16 x 4096: 8.3 and 7.4). A wavefront requests two blocks at a time if K has
+// them (16 x 4096: 7.4, one at a time 8.8; at K = 2048, where every second
+// would be for nothing, 5.6 and 4.5).
+//
+// Above, while one round of workgroups, one a compute unit, covers the product:
+// the stream with the fewest rows and features a workgroup that does so, since
+// a compute unit's time goes with what it reads: 32 x 16 7.1 (24 x 4096), 32 x
+// 32 8.2, 48 x 32 10.0, 64 x 32 11.9, 48 x 64 12.7, 64 x 64 14.7; the smallest
+// tile 15.4.
 //
 // Tiles: the kind whose rounds of workgroups cost least. A round, with as many
 // workgroups as fit the chip at once:
@@ -599,24 +644,33 @@ static bool quantises_inside(int64_t M) { return M <= 16; }
 //   fp32 output   128 x 256   256  69     128 x 128   256  41     64 x 64   256  22
 // (2048 x 4096: 56 / 39 / 41 / 49 / 63; 1000 x 4096: 54 / 34 / 32 / 26 / 33;
 // 200 x 4096: 52 / 33 / 31 / 23 / 16; 8192 x 8192: 240 / 283 / 292 / 367 / 432.)
+template <int FN, bool XQ, bool BF16>
+static void launch_16(const LinearArgs& p, hipStream_t s) {
+  if (p.K > 16 * kLinB)
+    launch_rows<1, FN, 16, 2, XQ, BF16>(p, s);
+  else
+    launch_rows<1, FN, 16, 1, XQ, BF16>(p, s);
+}
+
 template <bool BF16>
 static void launch_form(const LinearArgs& p, hipStream_t s) {
+  constexpr int kUnits = 256;  // compute units
   const auto blocks = [&](int tm, int tn) {
     return ((p.M + tm - 1) / tm) * (int64_t)((p.N + tn - 1) / tn);
   };
   if (p.M <= 16) {
-    const bool wide = blocks(16, 32) >= 256;
-    if (p.x)
-      return wide ? launch_rows<1, 2, 16, 1, true, BF16>(p, s)
-                  : launch_rows<1, 1, 8, 2, true, BF16>(p, s);
-    return wide ? launch_rows<1, 2, 8, 4, false, BF16>(p, s)
-                : launch_rows<1, 1, 8, 2, false, BF16>(p, s);
+    if (blocks(16, 16) > kUnits)
+      return p.x ? launch_16<2, true, BF16>(p, s) : launch_16<2, false, BF16>(p, s);
+    return p.x ? launch_16<1, true, BF16>(p, s) : launch_16<1, false, BF16>(p, s);
   }
-  if (p.M <= 32)
-    return blocks(32, 32) >= 256 ? launch_rows<2, 2, 16, 2, false, BF16>(p, s)
-                                 : launch_rows<2, 1, 8, 2, false, BF16>(p, s);
-  if (blocks(32, 32) <= 256 && p.K >= 16 * kLinB)
-    return launch_rows<2, 2, 16, 2, false, BF16>(p, s);
+  if (blocks(32, 16) <= kUnits)
+    return p.K > 16 * kLinB ? launch_rows<2, 1, 16, 2, false, BF16>(p, s)
+                            : launch_rows<2, 1, 16, 1, false, BF16>(p, s);
+  if (blocks(32, 32) <= kUnits) return launch_rows<2, 2, 8, 1, false, BF16>(p, s);
+  if (blocks(48, 32) <= kUnits) return launch_rows<3, 2, 8, 1, false, BF16>(p, s);
+  if (blocks(64, 32) <= kUnits) return launch_rows<4, 2, 8, 1, false, BF16>(p, s);
+  if (blocks(48, 64) <= kUnits) return launch_rows<3, 4, 8, 1, false, BF16>(p, s);
+  if (blocks(64, 64) <= kUnits) return launch_rows<4, 4, 8, 1, false, BF16>(p, s);
   const auto cost = [&](int tm, int tn, int round, int us) {
     return (blocks(tm, tn) + round - 1) / round * us;
   };
