@@ -182,9 +182,7 @@ __device__ __forceinline__ void linear_tile_of(int b, int tiles_m, int tiles_n, 
 // the exchange left out 7.3).
 //   XQ: the activations are bf16 rows of x, quantised as they are read: a
 // lane holds 32 of a row's 128 columns, the row's four lanes agree on the
-// largest magnitude, and the conversion instruction does the rest. Each
-// workgroup repeats that work for its own features, which up to 16 rows is
-// cheaper than a launch of its own (measured below).
+// largest magnitude, and the conversion instruction does the rest.
 __device__ __forceinline__ i32x8_t quantised_operand(const uint4 (&v)[4], int& e) {
   uint32_t m = 0;
 #pragma unroll
@@ -618,8 +616,18 @@ static void launch_rows(const LinearArgs& p, hipStream_t s) {
   linear_rows<FM, FN, W, U, XQ, BF16><<<grid, 64 * W, 0, s>>>(p);
 }
 
-// Whether the product quantises bf16 rows itself (one launch).
-static bool quantises_inside(int64_t M) { return M <= 16; }
+constexpr int kUnits = 256;  // compute units
+static int64_t tiles_of(int64_t M, int N, int tm, int tn) {
+  return (M + tm - 1) / tm * ((N + tn - 1) / tn);
+}
+
+// Whether the product quantises bf16 rows itself. Its workgroups then read x at
+// two bytes and each repeat the conversion for their own features: K = 1024 +
+// 1.1 us, 2048 + 2.0, 4096 + 3.7 (77 x 2112), where a launch of the quantiser
+// takes 3.1 and the gap to the next one 1 (measured up to 128 rows).
+static bool quantises_inside(int64_t M, int N, int K) {
+  return M <= 16 || (M <= 128 && K <= 32 * kLinB && tiles_of(M, N, 32, 32) <= kUnits);
+}
 
 // Which kernel a product runs on. Times in us on one MI355X for K = 4096 (they
 // go with K), weights not in any cache.
@@ -654,19 +662,19 @@ static void launch_16(const LinearArgs& p, hipStream_t s) {
 
 template <bool BF16>
 static void launch_form(const LinearArgs& p, hipStream_t s) {
-  constexpr int kUnits = 256;  // compute units
-  const auto blocks = [&](int tm, int tn) {
-    return ((p.M + tm - 1) / tm) * (int64_t)((p.N + tn - 1) / tn);
-  };
+  const auto blocks = [&](int tm, int tn) { return tiles_of(p.M, p.N, tm, tn); };
   if (p.M <= 16) {
     if (blocks(16, 16) > kUnits)
       return p.x ? launch_16<2, true, BF16>(p, s) : launch_16<2, false, BF16>(p, s);
     return p.x ? launch_16<1, true, BF16>(p, s) : launch_16<1, false, BF16>(p, s);
   }
   if (blocks(32, 16) <= kUnits)
-    return p.K > 16 * kLinB ? launch_rows<2, 1, 16, 2, false, BF16>(p, s)
-                            : launch_rows<2, 1, 16, 1, false, BF16>(p, s);
-  if (blocks(32, 32) <= kUnits) return launch_rows<2, 2, 8, 1, false, BF16>(p, s);
+    return p.x               ? launch_rows<2, 1, 16, 1, true, BF16>(p, s)
+           : p.K > 16 * kLinB ? launch_rows<2, 1, 16, 2, false, BF16>(p, s)
+                              : launch_rows<2, 1, 16, 1, false, BF16>(p, s);
+  if (blocks(32, 32) <= kUnits)
+    return p.x ? launch_rows<2, 2, 8, 1, true, BF16>(p, s)
+               : launch_rows<2, 2, 8, 1, false, BF16>(p, s);
   if (blocks(48, 32) <= kUnits) return launch_rows<3, 2, 8, 1, false, BF16>(p, s);
   if (blocks(64, 32) <= kUnits) return launch_rows<4, 2, 8, 1, false, BF16>(p, s);
   if (blocks(48, 64) <= kUnits) return launch_rows<3, 4, 8, 1, false, BF16>(p, s);
@@ -731,7 +739,7 @@ static moe_status linear_call(LinearArgs p, moe_dtype out_dtype, void* workspace
     if (workspace_bytes < need || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
       return MOE_ERR_WORKSPACE;
   }
-  if (p.x && !quantises_inside(p.M)) {
+  if (p.x && !quantises_inside(p.M, p.N, p.K)) {
     uint8_t* codes = static_cast<uint8_t*>(workspace);
     uint8_t* exps = codes + al256((size_t)p.M * p.K);
     if (launch_quant_act(p.x, p.M, p.K, codes, exps, s, p.ld_x) != hipSuccess) return MOE_ERR_HIP;
@@ -754,7 +762,7 @@ extern "C" {
 size_t moe_linear_workspace_bytes(int64_t rows, int32_t out_features, int32_t in_features,
                                   int32_t x_is_codes) {
   if (check_sizes(rows, out_features, in_features) != MOE_OK || rows == 0) return 0;
-  if (x_is_codes || quantises_inside(rows)) return 0;
+  if (x_is_codes || quantises_inside(rows, out_features, in_features)) return 0;
   return al256((size_t)rows * in_features) + al256((size_t)rows * (in_features / kLinB));
 }
 
