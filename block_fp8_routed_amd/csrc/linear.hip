@@ -648,10 +648,12 @@ static bool quantises_inside(int64_t M, int N, int K) {
 // workgroups as fit the chip at once:
 //   bf16 output   256 x 256   256 workgroups  62     128 x 256   256  39
 //                 128 x 128   512 (two a compute unit)  41, or 256 with a
-//                             deeper ring  26          64 x 64    512  16
-//   fp32 output   128 x 256   256  69     128 x 128   256  41     64 x 64   256  22
-// (2048 x 4096: 56 / 39 / 41 / 49 / 63; 1000 x 4096: 54 / 34 / 32 / 26 / 33;
-// 200 x 4096: 52 / 33 / 31 / 23 / 16; 8192 x 8192: 240 / 283 / 292 / 367 / 432.)
+//                             deeper ring  26          64 x 64    512  20
+//   fp32 output   128 x 256   256  69     128 x 128   256  41     64 x 64   512  29
+// (bf16: 2048 x 4096: 56 / 39 / 41 / 49 / 63; 1000 x 4096: 54 / 34 / 32 / 26 /
+// 38; 500 x 4096: 64 x 64 21; 8192 x 8192: 240 / 283 / 292 / 367 / 432. fp32:
+// 2048 x 4096: 69 / 82 / 88; 1000 x 4096: 66 / 44 / 50; 300 x 4096: 128 x 128
+// 41, 64 x 64 28; 8192 x 8192: 535 / 642 / 707.)
 template <int FN, bool XQ, bool BF16>
 static void launch_16(const LinearArgs& p, hipStream_t s) {
   if (p.K > 16 * kLinB)
@@ -683,7 +685,7 @@ static void launch_form(const LinearArgs& p, hipStream_t s) {
     return (blocks(tm, tn) + round - 1) / round * us;
   };
   if constexpr (BF16) {
-    const int64_t t[] = {cost(64, 64, 512, 16), cost(128, 128, 256, 26), cost(128, 128, 512, 41),
+    const int64_t t[] = {cost(64, 64, 512, 20), cost(128, 128, 256, 26), cost(128, 128, 512, 41),
                          cost(128, 256, 256, 39), cost(256, 256, 256, 62)};
     int best = 0;
     for (int i = 1; i < 5; ++i)
@@ -696,9 +698,9 @@ static void launch_form(const LinearArgs& p, hipStream_t s) {
       default: return launch_tile<256, 256, 2, 4, 2, BF16>(p, s);
     }
   } else {
-    const int64_t t0 = cost(64, 64, 256, 22), t1 = cost(128, 128, 256, 41),
+    const int64_t t0 = cost(64, 64, 512, 29), t1 = cost(128, 128, 256, 41),
                   t2 = cost(128, 256, 256, 69);
-    if (t0 <= t1 && t0 <= t2) return launch_tile<64, 64, 2, 2, 4, BF16>(p, s);
+    if (t0 <= t1 && t0 <= t2) return launch_tile<64, 64, 2, 2, 2, BF16>(p, s);
     if (t1 <= t2) return launch_tile<128, 128, 4, 2, 2, BF16>(p, s);
     launch_tile<128, 256, 2, 4, 3, BF16>(p, s);
   }

@@ -168,6 +168,68 @@ def test_activation_range(M):
     run(M, 160, K, x=x, scales=s)
 
 
+# products of more than 256 tiles of 64 x 64: one of every kind of tile for each
+# output type, with part-full tiles on both edges
+TILES = [(300, 4000), (700, 5000), (17300, 300), (2000, 4000), (2200, 5000)]
+
+
+@pytest.mark.parametrize("M,N", TILES)
+@pytest.mark.parametrize("K", [128, 384])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_tiles(M, N, K, out_dtype):
+    run(M, N, K, out_dtype, bias=True, seed=M + K, ld_x=8, ld_out=8 if K == 128 else 1)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 4000, 1152), (300, 4000, 4224), (700, 5000, 1280),
+                                   (2000, 4000, 640), (2200, 5000, 512)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_tiles_of_more_blocks(M, N, K, out_dtype):
+    run(M, N, K, out_dtype, seed=M + K)
+
+
+@pytest.mark.parametrize("M,N", [(300, 4000), (700, 5000), (2200, 5000)])
+def test_tiles_repeat_and_replay(M, N):
+    import block_fp8_routed_amd as moe
+    K = 768
+    w, s = (torch.from_numpy(a).cuda() for a in weights(N, K, 6))
+    x = rows(M, K, 6).cuda()
+    codes, exps = moe.moe_quantize_act_e4m3(x)
+    buf = torch.empty(exps.numel() + 4, dtype=torch.uint8, device="cuda")
+    for out_dtype in (torch.bfloat16, torch.float32):
+        want = moe.moe_linear(x, w, s, out_dtype=out_dtype)
+        for skip in (0, 1, 2):  # exponents at any address
+            moved = buf[skip:skip + exps.numel()].view(exps.shape)
+            moved.copy_(exps)
+            assert torch.equal(moe.moe_linear_e4m3(codes, moved, w, s, out_dtype=out_dtype), want)
+        out = torch.empty_like(want)
+        ws = torch.empty(moe.linear_workspace_bytes(M, N, K, False), dtype=torch.uint8,
+                         device="cuda")
+        moe.moe_linear(x, w, s, out=out, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_linear(x, w, s, out=out, workspace=ws)
+        x0 = x.clone()
+        for i in range(4):
+            x.copy_(x0 * (i + 1))
+            out.zero_()
+            graph.replay()
+            eager = moe.moe_linear(x, w, s, out_dtype=out_dtype)
+            torch.cuda.synchronize()
+            assert torch.equal(out, eager), f"replay {i}"
+        x.copy_(x0)
+
+
+# the stream's forms: one round of 32 x 16, 32 x 32, 48 x 32, 64 x 32, 48 x 64, 64 x 64
+@pytest.mark.parametrize("M,N", [(31, 4090), (33, 2000), (90, 2600), (96, 3900), (130, 3300),
+                                 (140, 5300), (255, 4090), (300, 3200), (20, 8100), (17, 9000),
+                                 (120, 4090), (60, 8000)])
+@pytest.mark.parametrize("K", [128, 1024, 2176, 4224])
+def test_stream_forms(M, N, K):
+    out_dtype = torch.float32 if (M + K // 128) % 2 else torch.bfloat16
+    run(M, N, K, out_dtype, bias=True, seed=M + K, ld_out=3)
+
+
 @pytest.mark.parametrize("M", [5, 70, 300])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
 def test_exponents_at_any_address(M, out_dtype):
