@@ -26,6 +26,11 @@
 // A token takes LPT lanes. Lane L of it owns nv consecutive experts L nv, L nv + 1,
 // ...: the lowest lane that holds a value then holds the lowest expert with
 // it, and where nv divides the group size a lane lies in one group.
+//
+// Bound by its own instructions (about 920 a wavefront for 512 experts, ten of
+// them in groups; reading the logits is a tenth of the time): 1 token of 512
+// experts 5.0 us, 48 tokens of 128 experts 5.8, 4096 of 512 13.8, 30001 of 160
+// 22.
 #include <cmath>
 #include <type_traits>
 
