@@ -376,13 +376,13 @@ moe_status moe_quantize_act_e4m3(const void* x, int64_t tokens, int32_t hidden, 
  * One linear layer whose weight is stored like the experts' (E4M3FN bytes
  * with one fp32 scale per 128 x 128 block), both operands in E4M3:
  *   out[t][n] = sum_k a[t][k] * dec(w[n][k]) * w_scales[n/128][k/128] (+ bias[n])
- * with a the activations quantised as moe_quantize_act_e4m3 describes.
- * summed in fp32 and rounded once to the output type. With fp32 output the
- * codes are multiplied as exact wider values; with bf16 output the FP8 matrix
- * instructions sum them, whose groups of eight products keep 13 bits below the
- * largest one (an error of at most 2^-10 of the terms' magnitudes, typically
- * 2^-15: below the output's own rounding). It is the
- * matrix product of MOE_PATH_MFMA_FP8 for a layer's dense projections and
+ * with a the activations quantised as moe_quantize_act_e4m3 describes, summed
+ * in fp32 and rounded once to the output type. With fp32 output, and at small
+ * sizes, the codes are multiplied as exact wider values; larger products with
+ * bf16 output are summed by the FP8 matrix instructions, whose groups of eight
+ * products keep 13 bits below the largest one (an error of at most 2^-10 of the
+ * terms' magnitudes, typically 2^-15: below the output's own rounding). It is
+ * the matrix product of MOE_PATH_MFMA_FP8 for a layer's dense projections and
  * feed-forward blocks (colizig page, "What this project is trying to prove":
  * natively block-FP8 checkpoints).
  *   x         [rows] rows of in_features bf16 values, finite, ld_x elements

@@ -181,6 +181,24 @@ def test_masks_and_ties_among_many_tokens(score):
         check(l, k, None, **rule)
 
 
+@pytest.mark.parametrize("E,k,groups,top", [(64, 4, 1, 1), (512, 10, 8, 4), (60, 16, 12, 4),
+                                            (160, 6, 8, 3), (9, 9, 1, 1), (128, 8, 64, 5)])
+@pytest.mark.parametrize("T", [7, 4200])
+def test_padded_batch(E, k, groups, top, T):
+    """Rows of padding, masked in every way, between ordinary ones; rows with a
+    few experts left."""
+    l = draw(T, E, 5)
+    l[1::2] = float("-inf")
+    l[3::8] = float("nan")
+    l[5::16] = torch.finfo(torch.float32).min
+    l[2::6, min(2, E - 1):] = float("-inf")
+    for score in ("softmax", "sigmoid"):
+        for rank in (1, 2):
+            rule = dict(score=score, groups=groups, top_groups=top, group_rank=rank)
+            check(l, k, bias(E, 3, 0.5), **rule)
+            check(l, k, None, renormalise=False, **rule)
+
+
 def test_no_tokens():
     import block_fp8_routed_amd as moe
     idx, gates = moe.moe_select_experts(torch.empty(0, 64, device="cuda"), 4, moe.Gating())
