@@ -200,13 +200,6 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t k) {
   return (uint32_t)__builtin_amdgcn_readlane((int)k, 63);
 }
 
-// Wave-wide maximum of floats (no NaN), uniform on return.
-__device__ __forceinline__ float wave_max_f32(float f) {
-  const uint32_t b = __float_as_uint(f);
-  const uint32_t m = wave_max_u32((b & 0x80000000u) ? ~b : (b | 0x80000000u));
-  return __uint_as_float((m & 0x80000000u) ? (m & 0x7fffffffu) : ~m);
-}
-
 __device__ __forceinline__ float silu(float z) { return z / (1.0f + __expf(-z)); }
 
 // 16-byte global load through the vector memory path.

@@ -723,9 +723,10 @@ static hipError_t launch_linear(const LinearArgs& p, bool bf16, hipStream_t s) {
 static moe_status check_sizes(int64_t M, int32_t N, int32_t K) {
   if (M < 0 || N <= 0 || K <= 0) return MOE_ERR_SHAPE;
   if (K % kLinB != 0) return MOE_ERR_UNSUPPORTED;
-  // 32-bit offsets within a tile, the tiles' count, and the quantiser's grid
+  // 32-bit offsets within a tile, fewer than 2^32 threads a grid (at most one
+  // for 64 outputs where there are many), and the quantiser's grid
   if (K > (1 << 22) || N > (1 << 24) || M > (1 << 20) ||
-      (M + 15) / 16 * ((N + 63) / 64) >= ((int64_t)1 << 31) ||
+      (M + 15) / 16 * ((N + 63) / 64) >= ((int64_t)1 << 27) ||
       M * (K / kLinB) >= ((int64_t)1 << 27))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

@@ -64,6 +64,13 @@ def test_select_refusals(kw, status):
     assert select(**kw) == status
 
 
+def test_grids_are_bounded():
+    """Calls whose grid would pass 2^32 threads are refused, not launched."""
+    assert select(tokens=1 << 26) == moe.MOE_ERR_UNSUPPORTED
+    assert linear(rows=1 << 20, n=1 << 18, k=128, ld_out=1 << 18,
+                  work_bytes=1 << 40) == moe.MOE_ERR_UNSUPPORTED
+
+
 def test_select_refuses_bad_enums():
     assert select(gating=raw(score=2)) == moe.MOE_ERR_SHAPE
     assert select(gating=raw(score=-1)) == moe.MOE_ERR_SHAPE
