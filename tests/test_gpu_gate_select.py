@@ -307,3 +307,28 @@ def test_another_stream():
     got = moe.moe_select_experts(dev, 8, moe.Gating(**SIGMOID8), stream=side)
     side.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("T", [1, 300, 4500])
+def test_choice_in_a_graph_and_on_two_streams(T):
+    import block_fp8_routed_amd as moe
+    gating = moe.Gating(score="sigmoid", groups=8, top_groups=4, group_rank=2, scale=2.5)
+    b = torch.from_numpy(bias(128)).cuda()
+    l = draw(T, 128, T).cuda()
+    moe.moe_select_experts(l, 8, gating, balance_bias=b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        idx, gates = moe.moe_select_experts(l, 8, gating, balance_bias=b)
+    l0 = l.clone()
+    for i in range(4):
+        l.copy_(l0.roll(i, 1))
+        graph.replay()
+        want = moe.moe_select_experts(l, 8, gating, balance_bias=b)
+        torch.cuda.synchronize()
+        assert torch.equal(idx, want[0]) and torch.equal(gates, want[1]), f"replay {i}"
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [moe.moe_select_experts(l, 8, gating, balance_bias=b, stream=s)
+           for _ in range(6) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) for g in got)
