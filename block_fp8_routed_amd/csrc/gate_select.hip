@@ -473,11 +473,15 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
       if (in && before == r.top_groups) lds.edge[1][base / 16] = make_float2(gs, mag);
       wave_lds_fence();
       const float2 k = lds.edge[0][base / 16], d = lds.edge[1][base / 16];
-      // (logits that are equal are equal scores, and so are two empty groups)
       const bool empty = k.x == -INFINITY && k.y == 0.f && d.y == 0.f;
+      // Equal logits on both sides of the cut are equal scores, of which the
+      // lower groups were kept. So may be other logits, above or below them, and
+      // then those take part in the tie.
+      const bool also = in && gs != k.x && close(fmaxf(gs, k.x), fminf(gs, k.x));
+      const bool tie = k.x == d.x && token_bits<LPT>(__ballot(also), base) == 0;
       const bool sure =
           empty || (k.x > -INFINITY &&
-                    (by_logit ? k.x == d.x || !close(k.x, d.x)
+                    (by_logit ? tie || (k.x != d.x && !close(k.x, d.x))
                               : k.x - d.x > 4.0f * eps + 0x1p-22f * fmaxf(k.y, d.y)));
       unsigned long long todo = __ballot(!sure);
       while (todo) {

@@ -1,0 +1,58 @@
+"""The gated choice where scores stop telling logits apart: the fp64 score of
+two different logits is then one number, and the lower index wins."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_gate_select import bias, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    import block_fp8_routed_amd as moe
+    moe.load()
+    yield
+    torch.cuda.synchronize()
+
+
+def group_rows(maxima, per, T, rest=-5.0):
+    """Rows whose groups hold one expert of the given logit (at a place that
+    moves from group to group) and the rest far below it, repeated to T rows."""
+    maxima = np.asarray(maxima, np.float32)
+    n, groups = maxima.shape
+    l = np.full((n, groups, per), np.float32(rest))
+    for g in range(groups):
+        l[:, g] = np.minimum(l[:, g], maxima[:, g:g + 1])
+        l[:, g, (3 * g + 1) % per] = maxima[:, g]
+    l = np.tile(l.reshape(n, groups * per), (-(-T // n), 1))[:T]
+    return torch.from_numpy(l)
+
+
+INF = float("inf")
+# equal best logits on both sides of the cut, and a group of another logit with
+# the same score: a smaller logit of a lower index, or a larger one of a higher
+EQUAL_SCORES = {
+    "sigmoid": [[39.5, -1.0, 40.0, 40.0], [40.0, 40.0, -1.0, 41.0], [50.0, -1.0, INF, INF],
+                [0.0, -3.0, 1e-18, 1e-18], [-2.0, 38.0, 60.0, 60.0], [1e-18, 1e-18, -3.0, 2e-18],
+                [-900.0, -2000.0, -800.0, -800.0], [40.0, 40.0, 40.0, 40.0],
+                [-1e-18, 0.0, 0.0, 0.0], [2.0, 3.0, 3.0, 1.0], [90.0, 40.0, 39.5, 90.0]],
+    "softmax": [[0.0, -5.0, 1e-18, 1e-18], [1e-18, 1e-18, -3.0, 2e-18],
+                [-900.0, 0.0, -800.0, -800.0], [-800.0, -800.0, 0.0, -790.0],
+                [5.0, 5.0, 5.0, 1.0], [2.0, 3.0, 3.0, 1.0], [50.0, -1.0, INF, INF]],
+}
+
+
+@pytest.mark.parametrize("T", [1, 3, 11, 4200])
+@pytest.mark.parametrize("per", [4, 8, 13])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_groups_of_equal_scores(score, per, T, dtype):
+    rows = EQUAL_SCORES[score]
+    for first in range(len(rows) if T == 1 else 1):
+        l = group_rows(rows[first:] + rows[:first], per, T, rest=-1e4).to(dtype)
+        for top in (1, 2, 3):
+            check(l, min(3, top * per), None, score=score, groups=4, top_groups=top, group_rank=1,
+                  renormalise=False)
