@@ -113,8 +113,8 @@ struct SliceLogits {
   }
 };
 
-// e^x in fp64 for x up to 709, within 2^-49: x = n ln 2 + r, |r| <= 0.35,
-// and the exponential series to r^12 (the rest is below 2^-50).
+// e^x in fp64 for x up to 710 (infinite from 709.78 on), within 2^-49: x = n ln 2
+// + r, |r| <= 0.35, and the exponential series to r^12 (the rest is below 2^-50).
 __device__ __forceinline__ double exp64(double x) {
   // ln 2 to 28 bits (n kLn2Hi is exact) and the rest
   constexpr double kLog2e = 0x1.71547652b82fep+0, kLn2Hi = 0x1.62e42fep-1,
@@ -246,9 +246,9 @@ __device__ __forceinline__ double softmax_sum(int nv, const float* raw, float to
 }
 
 // An expert's score from its logit (-inf: masked); softmax: not yet divided
-// by the sum.
+// by the sum. A sigmoid is 0 where its exponential leaves fp64's range.
 __device__ __forceinline__ double score64(const GateRule& r, float logit, float top) {
-  const double x = r.softmax ? (double)logit - (double)top : fmin(-(double)logit, 709.0);
+  const double x = r.softmax ? (double)logit - (double)top : fmin(-(double)logit, 710.0);
   const double e = exp64(x);
   const double s = r.softmax ? e : 1.0 / (1.0 + e);
   return logit > kMaskedLogit ? s : 0.0;

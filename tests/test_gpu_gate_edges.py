@@ -56,3 +56,32 @@ def test_groups_of_equal_scores(score, per, T, dtype):
         for top in (1, 2, 3):
             check(l, min(3, top * per), None, score=score, groups=4, top_groups=top, group_rank=1,
                   renormalise=False)
+
+
+@pytest.mark.parametrize("T", [1, 6, 4200])
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_sigmoid_of_logits_far_below_zero(groups, renormalise, T):
+    """1 / (1 + e^-l) leaves fp64's range below l = -709.8 and is 0 there: such
+    experts, finite masks of -1e4 or -1e9 among them, get no share of the gates."""
+    E = 32
+    rng = np.random.default_rng(4)
+    l = np.full((12, E), np.float32(-1e9))
+    l[1] = -1e4
+    l[2] = -720.0
+    l[3] = -705.0
+    l[4] = -5000.0
+    l[4, 9] = -705.0
+    l[5] = rng.choice(np.float32([-705, -720, -1e4, -1e9]), E)
+    l[6] = rng.choice(np.float32([-709.0, -709.5, -708.25]), E)
+    l[7, 3] = 1.5
+    l[8] = -800.0 - np.arange(E)
+    l[9] = -700.0 - 0.125 * np.arange(E)
+    l[10, ::5] = -3.0e38
+    l[11] = -3.0e38
+    for first in range(12 if T == 1 else 1):
+        rows = torch.from_numpy(np.tile(np.roll(l, -first, 0), (-(-T // 12), 1))[:T])
+        rule = dict(score="sigmoid", groups=groups, top_groups=max(1, groups // 2),
+                    group_rank=1, renormalise=renormalise, scale=2.5)
+        check(rows, 6, None, **rule)
+        check(rows, 6, bias(E, 2, 0.5), **rule)
