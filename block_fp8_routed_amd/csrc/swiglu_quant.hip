@@ -58,16 +58,20 @@ __global__ __launch_bounds__(256) void swiglu_quant_kernel(const uint16_t* __res
     h[j] = swiglu1(g[j], u[j]);
     m = max(m, __float_as_uint(h[j]) & 0x7fffffffu);
   }
-  // Gates below -69 (e^69 = 2^99.5), where the reciprocal nears its end, and
-  // infinite or NaN values redo their wavefront in full (an infinite h counts
-  // as the largest finite value).
+  // Gates down from -69 (e^69 = 2^99.5), where the reciprocal nears its end, and
+  // infinite or NaN values are computed again in full (an infinite h counts as the
+  // largest finite value). Each value goes by its own gate and result, so that
+  // neighbours in the wavefront, which may be other rows, have no say in it.
   uint2 nans = make_uint2(0u, 0u);  // 0x7f at the bytes whose h is NaN
   if (__ballot(m >= 0x7f800000u || bf16x8_max_bits(gw) >= 0xc28au)) {
     m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float v = g[j] / (1.0f + expf(-g[j])) * u[j];
-      if (fabsf(v) > FLT_MAX) v = copysignf(FLT_MAX, v);
+      float v = h[j];
+      if (g[j] <= -69.0f || !(fabsf(v) <= FLT_MAX)) {
+        v = g[j] / (1.0f + expf(-g[j])) * u[j];
+        if (fabsf(v) > FLT_MAX) v = copysignf(FLT_MAX, v);
+      }
       const uint32_t bits = __float_as_uint(v), mag = bits & 0x7fffffffu;
       const bool nan = mag > 0x7f800000u;
       h[j] = nan ? 0.f : v;

@@ -426,7 +426,8 @@ moe_status moe_linear_e4m3(const uint8_t* codes, const uint8_t* exps, const uint
  *   exps    [tokens][inter/128] E8M0 bytes (written)
  * A NaN h (from a NaN or infinite input) becomes the NaN byte 0x7F and does
  * not take part in its block's scale; an h beyond fp32 counts as fp32's
- * largest value. inter must be a multiple of 128 (else MOE_ERR_UNSUPPORTED);
+ * largest value. A value's code depends on its own gate and up value and on its
+ * block's scale, a row's results on no other row. inter must be a multiple of 128 (else MOE_ERR_UNSUPPORTED);
  * tokens == 0 enqueues nothing. */
 moe_status moe_swiglu_quantize_e4m3(const void* gate_up, int64_t ld, int64_t tokens,
                                     int32_t inter, uint8_t* codes, uint8_t* exps, void* stream);
