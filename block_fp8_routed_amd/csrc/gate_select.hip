@@ -722,8 +722,8 @@ extern "C" moe_status moe_select_experts(const void* logits, moe_dtype dtype, in
   GateRule r;
   const moe_status st = gate_rule(gating, experts, top_k, &r);
   if (st != MOE_OK) return st;
-  if (experts > kMaxExperts || top_k > kMaxTopK || tokens >= ((int64_t)1 << 26))
-    return MOE_ERR_UNSUPPORTED;  // (a grid has fewer than 2^32 threads)
+  if (experts > kMaxExperts || top_k > kMaxTopK || tokens > kMaxGateTokens)
+    return MOE_ERR_UNSUPPORTED;
   if (!logits || !topk_idx || !gates) return MOE_ERR_NULL;
   if (tokens == 0) return MOE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -7,6 +7,8 @@
 namespace moe {
 
 constexpr int kMaxGroups = 64;  // a group's score is made by at least one lane
+// four tokens a workgroup of 256 threads, fewer than 2^32 threads a grid
+constexpr int64_t kMaxGateTokens = ((int64_t)1 << 26) - 4;
 constexpr float kMaskedLogit = -3.3e38f;  // at or below: the expert is masked
 
 // moe_gating, checked and completed for one layer.

@@ -222,7 +222,7 @@ static moe_status forward(const void* x, const float* router_w, const float* rou
     st = gate_rule(gating, d.E, d.k, &rule);
     if (st != MOE_OK) return st;
     // the single-launch layer selects by the logits alone
-    if (cfg->path == MOE_PATH_GEMV_FUSED) return MOE_ERR_UNSUPPORTED;
+    if (cfg->path == MOE_PATH_GEMV_FUSED || d.T > kMaxGateTokens) return MOE_ERR_UNSUPPORTED;
     // the gated choice is a launch of its own, which does not clear the
     // fold's counters
     d.fold_combine = false;
@@ -305,6 +305,7 @@ moe_status moe_route_gated(const void* x, const float* router_w, const float* ro
   GateRule rule;
   st = gate_rule(gating, d.E, d.k, &rule);
   if (st != MOE_OK) return st;
+  if (d.T > kMaxGateTokens) return MOE_ERR_UNSUPPORTED;
   if (!x || !router_w || !topk_idx || !gates) return MOE_ERR_NULL;
   if (d.T == 0) return MOE_OK;
   st = check_workspace(d, workspace, workspace_bytes_);

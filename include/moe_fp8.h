@@ -308,8 +308,8 @@ typedef struct {
  *   logits       [tokens] rows of `experts` values of `dtype`, ld elements apart
  *   balance_bias [experts] fp32 (finite), or NULL for none
  *   topk_idx     [tokens][top_k] int32, gates [tokens][top_k] fp32 (written)
- * experts 1 .. 1024, top_k 1 .. min(experts, 16), tokens below 2^26. No
- * workspace. */
+ * experts 1 .. 1024, top_k 1 .. min(experts, 16), tokens up to 2^26 - 4 (here
+ * and in the two calls below). No workspace. */
 moe_status moe_select_experts(const void* logits, moe_dtype dtype, int64_t ld,
                               const float* balance_bias, const moe_gating* gating,
                               int64_t tokens, int32_t experts, int32_t top_k, int32_t* topk_idx,
