@@ -74,10 +74,15 @@ __device__ __forceinline__ f16x8_t widen(int lo, int hi) {
 // l / 16 (any 32, the same for both operands); the result's column l % 16 (B's
 // row) at rows 4 (l / 16) + v. Byte SEL of scale is the E8M0 byte of B's row;
 // s is the weights' block scale, premultiplied as block_scale() does.
-// A sum of 128 code products reaches 2^25 and the activations' scale 2^120, so
-// a factor is held back until s joins: the FP8 instruction's A operand has the
-// constant scale 2^-kHold; the fp16 form takes what is above 2^100 out of 2^e.
-constexpr int kHold = 18;
+// The sums must neither overflow nor fall below what fp32 holds before s joins. With
+// codes and exponents as the quantisers write them (codes of 256 at most at the
+// exponent 120, which takes the ends of bf16 and fp32; 448 below) a sum of 128
+// products stays below 2^143.81, so the FP8 instruction's A operand has the
+// constant scale 2^-kHold: 2^127.81. At the other end its smallest product,
+// 2^-18 2^-127, is then cut at 2^-149: a block of exponent -127 errs by 2^-150
+// 2^kHold s. The fp16 form takes what is above 2^100 out of 2^e and loses nothing
+// (2^-18 2^-127 is a subnormal fp32 value, and kept).
+constexpr int kHold = 16;
 template <bool BF16>
 __device__ __forceinline__ float block_scale(float s) {
   return BF16 ? s * (float)(1 << kHold) : s;
