@@ -46,8 +46,8 @@ __device__ __forceinline__ int act_exponent(float amax) {
 // Eight bf16 values (an uint4) to eight E4M3 bytes of v * 2^-e, |v| <= 448 *
 // 2^e: gfx950's scaled conversion, which takes the scale 2^e itself. It gives
 // e4m3_rne's byte for every bf16 value under every exponent -127 .. 120 that
-// its block can have (checked on the card over all of them; likewise
-// e4m3x8_of_f32 for fp32 values).
+// its block can have (tests/test_gpu_e4m3_conversions.py runs them all against the
+// oracle's rounding, and samples of fp32 values through e4m3x8_of_f32).
 __device__ __forceinline__ uint2 e4m3x8_of_bf16(uint4 w, int e) {
   typedef short i16x2 __attribute__((ext_vector_type(2)));
   const float s = __builtin_ldexpf(1.0f, e);
