@@ -9,13 +9,14 @@
 // multiplies the instruction's fp32 result as it is added to the running sum.
 // The instruction sums eight consecutive products of a lane on one grid, 2^-13
 // of the largest (measured: 2^16 + 2^3 is exact, 2^16 + 2^2 loses the second
-// term), so a sum errs by at most 2^-10 of its terms' magnitudes and, as the
-// cuts go either way, by a few 2^-15 in norm: far below the output's own step
-// of 2^-8.
+// term), so a sum errs by at most 2^-10 of its terms' magnitudes. Towards zero, the
+// cuts of terms of either sign go either way: 6e-5 of the result in norm (measured
+// at K = 512 and 1024), where the output's rounding is 1.7e-3. An element whose
+// terms cancel has no bound relative to itself.
 //
-// (What follows may see the cuts through its own rounding: an E4M3 code of a
-// result near a midpoint falls to either side. The exact form below would take
-// 535 us where this one takes 240.)
+// (What follows may see the cuts through its own rounding: a bf16 value or an
+// E4M3 code near a midpoint falls to either side. The exact form below would take
+// 535 us where this one takes 240 to 260; fp32 output is the caller's way to it.)
 //
 // fp32 output: that error would be the result's, so the codes are widened to
 // fp16 in registers (exact) and go through v_mfma_f32_16x16x32_f16, which
@@ -78,10 +79,11 @@ __device__ __forceinline__ f16x8_t widen(int lo, int hi) {
 // codes and exponents as the quantisers write them (codes of 256 at most at the
 // exponent 120, which takes the ends of bf16 and fp32; 448 below) a sum of 128
 // products stays below 2^143.81, so the FP8 instruction's A operand has the
-// constant scale 2^-kHold: 2^127.81. At the other end its smallest product,
-// 2^-18 2^-127, is then cut at 2^-149: a block of exponent -127 errs by 2^-150
-// 2^kHold s. The fp16 form takes what is above 2^100 out of 2^e and loses nothing
-// (2^-18 2^-127 is a subnormal fp32 value, and kept).
+// constant scale 2^-kHold: 2^127.81. At the other end each of its sixteen groups of
+// products is then cut at 2^-149, where the smallest product of a block of exponent
+// e is 2^-18 2^(e - kHold): below e = -115 a block may lose 2^-145 2^kHold s. The
+// fp16 form takes what is above 2^100 out of 2^e and loses nothing (2^-18 2^-127
+// is a subnormal fp32 value, and kept).
 constexpr int kHold = 16;
 template <bool BF16>
 __device__ __forceinline__ float block_scale(float s) {
