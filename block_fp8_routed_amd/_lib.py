@@ -522,18 +522,27 @@ def _empty(like: torch.Tensor, shape, dtype, stream):
         return like.new_empty(shape, dtype=dtype)
 
 
+def _public_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current stream's handle and device. torch's own functions for them, where
+# this torch has them: the public ones wrap these and take as long as the rest of
+# a small call's checks.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _enqueue(fn, name: str, index: int, stream, *args):
     """Calls the C function `fn` on GPU `index` and the given stream or that
-    GPU's current one. (The raw handles are what torch.cuda.current_stream() and
-    current_device() wrap; the wrappers take as long as the rest of a small
-    call's checks.)"""
+    GPU's current one."""
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(index)
+        s = _raw_stream(index)
     elif stream.device_index == index:
         s = stream.cuda_stream
     else:
         raise ValueError("stream must be on the tensors' GPU")
-    if index == torch._C._cuda_getDevice():
+    if index == _raw_device():
         st = fn(*args, s)
     else:
         with torch.cuda.device(index):
