@@ -85,3 +85,53 @@ def test_sigmoid_of_logits_far_below_zero(groups, renormalise, T):
                     group_rank=1, renormalise=renormalise, scale=2.5)
         check(rows, 6, None, **rule)
         check(rows, 6, bias(E, 2, 0.5), **rule)
+
+
+@pytest.mark.parametrize("tokens", [4096, 4099])
+def test_route_gated_with_tokens_that_share_a_wavefront(tokens):
+    """Long batches on the 128-expert layer: four tokens a wavefront read the
+    router's partial logits, and the finished ones are handed back."""
+    import block_fp8_routed_amd as moe
+    import oracle
+    import workloads as W
+    from parity import DevLayer
+    from test_gpu_gate_select import SIGMOID8, check_gates
+    layer = DevLayer(W.CONFIGS["c1"], tokens=tokens)
+    s = layer.shape
+    bal = torch.from_numpy(bias(s.experts)).cuda()
+    idx, gates, logits = moe.moe_route_gated(layer.x, layer.router_w, s.top_k,
+                                             moe.Gating(**SIGMOID8), s.inter, s.block,
+                                             router_bias=layer.bias, balance_bias=bal,
+                                             with_logits=True)
+    ref_idx, ref_g = oracle.gated_choice(logits.double().cpu().numpy(), s.top_k,
+                                         balance=bal.cpu().numpy(), **SIGMOID8)
+    assert (idx.cpu().numpy() == ref_idx).all()
+    check_gates(gates, ref_g, f"T={tokens}")
+    _, _, plain = layer.route(with_logits=True)
+    assert torch.equal(plain, logits)
+
+
+@pytest.mark.parametrize("name,tokens", [("c1", 40), ("c3", 64)])
+def test_forward_gated_in_fp8(name, tokens):
+    """The FP8 expert passes behind the gated choice: each token's result is that
+    of the plain bf16 passes on the same choice, but for the quantisation of x and
+    h (2^-4 a value at most, of random sign: a few percent in norm)."""
+    import block_fp8_routed_amd as moe
+    import workloads as W
+    from parity import DevLayer
+    from test_gpu_gate_select import SIGMOID8
+    layer = DevLayer(W.CONFIGS[name], tokens=tokens)
+    s = layer.shape
+    gating = moe.Gating(**dict(SIGMOID8, groups=4, top_groups=2))
+    bal = torch.from_numpy(bias(s.experts)).cuda()
+
+    def call(path):
+        return moe.moe_forward_gated(layer.x, layer.router_w, layer.bank, s.top_k, s.block, gating,
+                                     shared=layer.shared, router_bias=layer.bias,
+                                     balance_bias=bal, path=path).double()
+
+    a, b, again = call("mfma_fp8"), call("mfma"), call("mfma_fp8")
+    assert torch.equal(a, again)
+    err = float((a - b).norm() / b.norm())
+    print(f"gated layer {name} in FP8: {err:.4f} of the bf16 passes in norm")
+    assert err < 0.1
