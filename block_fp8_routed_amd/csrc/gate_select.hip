@@ -477,8 +477,11 @@ __device__ __forceinline__ bool choose_fast(const GateRule& r, const float (&v)[
       // Equal logits on both sides of the cut are equal scores, of which the
       // lower groups were kept. So may be other logits, above or below them, and
       // then those take part in the tie.
-      const bool also = in && gs != k.x && close(fmaxf(gs, k.x), fminf(gs, k.x));
-      const bool tie = k.x == d.x && token_bits<LPT>(__ballot(also), base) == 0;
+      bool tie = by_logit && k.x == d.x;
+      if (__ballot(tie)) {
+        const bool also = in && gs != k.x && close(fmaxf(gs, k.x), fminf(gs, k.x));
+        tie = tie && token_bits<LPT>(__ballot(also), base) == 0;
+      }
       const bool sure =
           empty || (k.x > -INFINITY &&
                     (by_logit ? tie || (k.x != d.x && !close(k.x, d.x))
