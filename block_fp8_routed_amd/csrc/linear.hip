@@ -22,8 +22,10 @@
 // fp16 in registers (exact) and go through v_mfma_f32_16x16x32_f16, which
 // keeps 2^-24 of the largest of eight products; the activations' scale is
 // applied to the instruction's result. Small batches take this form for both
-// output types. Its conversions bound the tiles: 96 of them and 32 matrix
-// instructions a stage of 32 x 64 outputs (8192 x 8192 x 4096: 1030 TFLOP/s).
+// output types. Its conversions bound the large tiles: 96 of them and 32 matrix
+// instructions a stage of 32 x 64 outputs (8192 x 8192 x 4096: 1030 TFLOP/s). A
+// single round of 128 x 128 tiles has some 8 us that do not go with K (16.5 us at
+// K = 1024, 41 at 4096): its ring holds one stage ahead.
 //
 // Weights are the instruction's A operand, so that a lane ends with four
 // consecutive output features of one row.

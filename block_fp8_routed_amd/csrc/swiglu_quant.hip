@@ -13,8 +13,8 @@
 // quotient are written out below, and the row of a chunk is found by a
 // multiplication. Sixteen lanes per block (a DPP row), eight columns of the
 // gate and of the up half per lane with one 16-byte load each. Measured: 8191 x
-// 4096 outputs 27.4 us (168 MB, 6.1 TB/s; 179 instructions a wavefront of 512
-// outputs), 4 x 1024 2.1 us (a launch).
+// 4096 outputs 27.7 us (168 MB, 6.1 TB/s; 179 instructions a wavefront of 512
+// outputs), 4 x 1024 2.0 us (a launch).
 #include <float.h>
 
 #include "device.hpp"
@@ -25,8 +25,9 @@ namespace moe {
 
 // silu(g) * u. e^-g = 2^t 2^r with t = -g log2(e) rounded to fp32 and r the
 // rest of the product (an fma against the same constant, plus the constant's
-// own rest), 2^r = 1 + r ln 2 to second order below 2^-45; the quotient is the
-// hardware reciprocal with one Newton step. About 2 ulps in all.
+// own rest), 2^r = 1 + r ln 2 (r grows with t's step: what is left out is 2^-42 at
+// |g| = 20 and 2^-38 at 69); the quotient is the hardware reciprocal with one
+// Newton step. About 2 ulps in all.
 __device__ __forceinline__ float swiglu1(float g, float u) {
   constexpr float kLog2e = 0x1.715476p+0f, kLog2eRest = 0x1.4ae0cp-26f, kLn2 = 0x1.62e43p-1f;
   const float t = -g * kLog2e;
