@@ -309,7 +309,7 @@ typedef struct {
  *   balance_bias [experts] fp32 (finite), or NULL for none
  *   topk_idx     [tokens][top_k] int32, gates [tokens][top_k] fp32 (written)
  * experts 1 .. 1024, top_k 1 .. min(experts, 16), tokens up to 2^26 - 4 (here
- * and in the two calls below). No workspace. */
+ * and in the two calls below). No workspace. The results overlap no input. */
 moe_status moe_select_experts(const void* logits, moe_dtype dtype, int64_t ld,
                               const float* balance_bias, const moe_gating* gating,
                               int64_t tokens, int32_t experts, int32_t top_k, int32_t* topk_idx,
@@ -403,7 +403,7 @@ moe_status moe_quantize_act_e4m3(const void* x, int64_t tokens, int32_t hidden, 
  *   bias      [out_features] fp32, or NULL for none
  *   out       [rows] rows of out_features values of out_dtype, ld_out elements
  *             apart (at least out_features); elements between rows are left
- *             alone
+ *             alone. It overlaps no input
  * moe_linear quantises x itself; its result has the same bits as
  * moe_quantize_act_e4m3 followed by moe_linear_e4m3. A row's result does not
  * depend on the other rows' values. in_features must be a multiple of 128
@@ -429,7 +429,7 @@ moe_status moe_linear_e4m3(const uint8_t* codes, const uint8_t* exps, const uint
  *   gate_up [tokens] rows of 2 * inter bf16 values (g, then u), ld elements
  *           apart (a multiple of 8, at least 2 * inter), 16-byte aligned
  *   codes   [tokens][inter] E4M3FN bytes (8-byte aligned, written)
- *   exps    [tokens][inter/128] E8M0 bytes (written)
+ *   exps    [tokens][inter/128] E8M0 bytes (written); neither overlaps gate_up
  * A NaN h (from a NaN or infinite input) becomes the NaN byte 0x7F and does
  * not take part in its block's scale; an h beyond fp32 counts as fp32's
  * largest value. A value's code depends on its own gate and up value and on its
