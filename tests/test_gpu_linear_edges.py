@@ -108,3 +108,21 @@ def test_cuts_of_the_fp8_instruction_in_norm(M, N, K):
     cut = (8 / 3) ** 0.5 * 2.0 ** -13
     print(f"norm {norm:.3e}, rounding {rounding:.3e}, cuts {max(norm ** 2 - rounding ** 2, 0) ** 0.5:.2e}")
     assert norm <= (rounding ** 2 + (2 * cut) ** 2) ** 0.5
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 300, 512), (16, 8192, 4096), (30, 300, 512), (77, 2112, 4096),
+                                   (300, 4000, 512), (700, 5000, 512), (2200, 5000, 512)])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_rows_beside_rows_that_are_not_finite(M, N, K, out_dtype):
+    """Rows of padding that hold NaN or infinities are no supported input, and
+    leave the others as they are."""
+    import block_fp8_routed_amd as moe
+    w, s = (torch.from_numpy(a).cuda() for a in weights(N, K, M))
+    x = rows(M, K, M).cuda()
+    want = moe.moe_linear(x, w, s, out_dtype=out_dtype)
+    for row, value in ((0, float("nan")), (M - 1, float("inf")), (M // 2, float("-inf"))):
+        bad = x.clone()
+        bad[row, ::3] = value
+        got = moe.moe_linear(bad, w, s, out_dtype=out_dtype)
+        keep = torch.arange(M, device="cuda") != row
+        assert torch.equal(got[keep], want[keep])
