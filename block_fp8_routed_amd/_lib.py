@@ -33,6 +33,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_forward", "moe_forward_static", "moe_forw
            "moe_select_experts", "moe_route_gated", "moe_forward_gated",
            "moe_linear_workspace_bytes", "moe_linear", "moe_linear_e4m3",
            "moe_swiglu_quantize_e4m3",
+           "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_dispatch_backward",
+           "moe_combine", "moe_combine_backward", "moe_linear_w4", "moe_grouped_linear_w4",
            "moe_status_string", "moe_version", "moe_set_wait_limit")
 (MOE_WS_TOPK, MOE_WS_GATES, MOE_WS_OFFSETS, MOE_WS_PAIR, MOE_WS_INV, MOE_WS_H, MOE_WS_H_EXPS,
  MOE_WS_Y, MOE_WS_Y_EXPS, MOE_WS_STATUS, MOE_WS_COUNT) = range(11)
@@ -144,8 +146,21 @@ def load() -> ctypes.CDLL:
     lib.moe_linear.argtypes = [P, I64, P, P, P, I64, I32, I32, P, I64, ctypes.c_int, P, SZ, P]
     lib.moe_linear_e4m3.argtypes = [P, P, P, P, P, I64, I32, I32, P, I64, ctypes.c_int, P, SZ, P]
     lib.moe_swiglu_quantize_e4m3.argtypes = [P, I64, I64, I32, P, P, P]
+    INT = ctypes.c_int
+    lib.moe_dispatch_workspace_bytes.argtypes = [I64, I32, I32]
+    lib.moe_dispatch_workspace_bytes.restype = SZ
+    lib.moe_dispatch.argtypes = [P, I64, INT, P, I64, I32, I32, I32, P, I64, P, P, P, P, SZ, P]
+    lib.moe_dispatch_backward.argtypes = [P, I64, I64, INT, P, I64, I32, I32, P, I64, INT, P]
+    lib.moe_combine.argtypes = [P, I64, I64, INT, P, P, P, I64, I64, I32, I32, P, I64, INT, P]
+    lib.moe_combine_backward.argtypes = [P, I64, INT, P, I64, I64, INT, P, P, I64, I32, I32, P,
+                                         I64, P, P]
+    lib.moe_linear_w4.argtypes = [P, I64, P, P, INT, P, P, I64, I32, I32, I32, I32, P, I64, INT, P]
+    lib.moe_grouped_linear_w4.argtypes = [P, I64, P, P, P, INT, P, P, I64, I32, I32, I32, I32, I32,
+                                          P, I64, INT, P]
     for name in ("moe_select_experts", "moe_route_gated", "moe_forward_gated", "moe_linear",
-                 "moe_linear_e4m3", "moe_swiglu_quantize_e4m3"):
+                 "moe_linear_e4m3", "moe_swiglu_quantize_e4m3", "moe_dispatch",
+                 "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_linear_w4",
+                 "moe_grouped_linear_w4"):
         getattr(lib, name).restype = ctypes.c_int
     lib.moe_workspace_region.argtypes = [cfgp, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t),
                                          ctypes.POINTER(ctypes.c_size_t)]
@@ -735,3 +750,191 @@ def moe_swiglu_quantize_e4m3(gate_up: torch.Tensor, stream=None):
     _enqueue((_lib or load()).moe_swiglu_quantize_e4m3, "moe_swiglu_quantize_e4m3", dev, stream,
              _addr(gate_up), ld, T, I, _addr(codes), _addr(exps))
     return codes, exps
+
+
+# ---- rows to their experts and back, and products with 4-bit weights ----
+def _matrix(t: torch.Tensor, cols: int, what: str):
+    """(moe_dtype, distance of rows) of a 2-D fp32 or bf16 tensor of `cols` columns."""
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None:
+        raise ValueError(f"{what} must be float32 or bfloat16")
+    ld = _rows(t, what)
+    if t.shape[1] != cols:
+        raise ValueError(f"{what} must have {cols} columns")
+    return dtype, ld
+
+
+def _result(out: Optional[torch.Tensor], like: torch.Tensor, rows: int, cols: int, dtype, stream,
+            what: str = "out"):
+    """(tensor, moe_dtype, distance of rows): `out`, or a new tensor of `dtype`."""
+    if out is None:
+        code = _DTYPES.get(dtype)
+        if code is None:
+            raise ValueError(f"unsupported dtype {dtype}")
+        return _empty(like, (rows, cols), dtype, stream), code, cols
+    code, ld = _matrix(out, cols, what)
+    if out.shape[0] != rows:
+        raise ValueError(f"{what} must have {rows} rows")
+    return out, code, ld
+
+
+def _slots(inv: torch.Tensor):
+    if inv.dim() != 2 or inv.dtype != torch.int32 or not inv.is_contiguous():
+        raise ValueError("inv must be a contiguous int32 tensor [tokens][top_k]")
+    return inv.shape
+
+
+@functools.lru_cache(maxsize=1024)
+def dispatch_workspace_bytes(tokens: int, top_k: int, experts: int) -> int:
+    """moe_dispatch_workspace_bytes (a function of the sizes alone)."""
+    return int(load().moe_dispatch_workspace_bytes(tokens, top_k, experts))
+
+
+def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, experts: int,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None):
+    """The rows of x [T][H] (fp32 or bf16; rows may lie apart) sorted by their
+    experts topk_idx [T][k] int32: (rows [T*k][H], offsets [experts+1], pair [T*k],
+    inv [T][k], all int32). Choices outside [0, experts) get no row (inv -1); rows
+    behind offsets[experts] are left as they were (pair -1)."""
+    dev = _place(x, topk_idx, out, workspace)
+    if x.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("x and topk_idx must be 2-D")
+    T, H = x.shape
+    dtype, ld = _matrix(x, H, "x")
+    k = topk_idx.shape[1]
+    _flat(topk_idx, (T, k), torch.int32, "topk_idx")
+    rows, code, ld_rows = _result(out, x, T * k, H, x.dtype, stream)
+    if code != dtype:
+        raise ValueError("out must have x's type")
+    offsets = _empty(topk_idx, (max(experts, 0) + 1,), torch.int32, stream)
+    pair = _empty(topk_idx, (T * k,), torch.int32, stream)
+    inv = _empty(topk_idx, (T, k), torch.int32, stream)
+    if workspace is None:
+        need = dispatch_workspace_bytes(T, k, experts)
+        if need:
+            workspace = _empty(x, (need,), torch.uint8, stream)
+    _enqueue((_lib or load()).moe_dispatch, "moe_dispatch", dev, stream, _addr(x), ld, dtype,
+             _addr(topk_idx), T, H, k, experts, _addr(rows), ld_rows, _addr(offsets), _addr(pair),
+             _addr(inv), _addr(workspace), _bytes(workspace))
+    return rows, offsets, pair, inv
+
+
+def moe_dispatch_backward(d_rows: torch.Tensor, inv: torch.Tensor, out_dtype=None,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of x from that of moe_dispatch's rows: each token's rows
+    summed, [T][H] of out_dtype (d_rows' type)."""
+    dev = _place(d_rows, inv, out)
+    if d_rows.dim() != 2:
+        raise ValueError("d_rows must be 2-D")
+    P, H = d_rows.shape
+    dtype, ld = _matrix(d_rows, H, "d_rows")
+    T, k = _slots(inv)
+    dx, code, ld_dx = _result(out, d_rows, T, H, out_dtype or d_rows.dtype, stream)
+    _enqueue((_lib or load()).moe_dispatch_backward, "moe_dispatch_backward", dev, stream,
+             _addr(d_rows), ld, P, dtype, _addr(inv), T, H, k, _addr(dx), ld_dx, code)
+    return dx
+
+
+def moe_combine(y: torch.Tensor, gates: torch.Tensor, inv: torch.Tensor,
+                shared: Optional[torch.Tensor] = None, out_dtype=None,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Each token's rows of y (moe_dispatch's order) times its gates [T][k] fp32,
+    summed, plus its row of `shared` ([T][H] of y's type): [T][H] of out_dtype
+    (y's type)."""
+    dev = _place(y, gates, inv, shared, out)
+    if y.dim() != 2:
+        raise ValueError("y must be 2-D")
+    P, H = y.shape
+    dtype, ld = _matrix(y, H, "y")
+    T, k = _slots(inv)
+    _flat(gates, (T, k), torch.float32, "gates")
+    ld_shared = 0
+    if shared is not None:
+        code, ld_shared = _matrix(shared, H, "shared")
+        if code != dtype or shared.shape[0] != T:
+            raise ValueError(f"shared must have y's type and {T} rows")
+    res, code, ld_out = _result(out, y, T, H, out_dtype or y.dtype, stream)
+    _enqueue((_lib or load()).moe_combine, "moe_combine", dev, stream, _addr(y), ld, P, dtype,
+             _addr(gates), _addr(inv), _addr(shared), ld_shared, T, H, k, _addr(res), ld_out, code)
+    return res
+
+
+def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, gates: torch.Tensor,
+                         inv: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of moe_combine: (d_y of y's shape and type, d_gates [T][k]
+    fp32). Rows of d_y without a token are left as they were; that of `shared` is
+    d_out."""
+    dev = _place(d_out, y, gates, inv, out)
+    if y.dim() != 2:
+        raise ValueError("y must be 2-D")
+    P, H = y.shape
+    dtype, ld = _matrix(y, H, "y")
+    d_dtype, ld_d = _matrix(d_out, H, "d_out")
+    T, k = _slots(inv)
+    if d_out.shape[0] != T:
+        raise ValueError(f"d_out must have {T} rows")
+    _flat(gates, (T, k), torch.float32, "gates")
+    d_y, code, ld_dy = _result(out, y, P, H, y.dtype, stream)
+    if code != dtype:
+        raise ValueError("out must have y's type")
+    d_gates = _empty(gates, (T, k), torch.float32, stream)
+    _enqueue((_lib or load()).moe_combine_backward, "moe_combine_backward", dev, stream,
+             _addr(d_out), ld_d, d_dtype, _addr(y), ld, P, dtype, _addr(gates), _addr(inv), T, H,
+             k, _addr(d_y), ld_dy, _addr(d_gates))
+    return d_y, d_gates
+
+
+def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, out_dtype, out):
+    """The checks and the call that both 4-bit products share; lead: () or (experts,)."""
+    if x.dim() != 2 or x.dtype != torch.bfloat16:
+        raise ValueError("x must be a 2-D bfloat16 tensor")
+    ld = _rows(x, "x")
+    M, K = x.shape
+    N = w.shape[-2]
+    _flat(w, (*lead, N, K // 2), torch.uint8, "w")
+    groups = w_scales.shape[-1]
+    scale = _DTYPES.get(w_scales.dtype)
+    if scale is None or groups == 0 or K % groups:
+        raise ValueError("w_scales must be float32 or bfloat16, its last dimension dividing x's")
+    _flat(w_scales, (*lead, N, groups), w_scales.dtype, "w_scales")
+    _flat(w_zeros, (*lead, N, groups), torch.uint8, "w_zeros")
+    _flat(bias, (*lead, N), torch.float32, "bias")
+    res, code, ld_out = _result(out, x, M, N // 2 if swiglu else N, out_dtype, stream)
+    _enqueue(getattr(_lib or load(), name), name, dev, stream, _addr(x), ld, *head, _addr(w),
+             _addr(w_scales), scale, _addr(w_zeros), _addr(bias), M, *lead, N, K, K // groups,
+             bool(swiglu), _addr(res), ld_out, code)
+    return res
+
+
+def moe_linear_w4(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+                  w_zeros: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                  swiglu: bool = False, out_dtype=torch.bfloat16,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x [T][K] bf16 (rows may lie apart) times the transpose of a 4-bit weight
+    (q - z) s: w [N][K/2] uint8 (the even column in the low four bits), w_scales
+    [N][K/group] fp32 or bf16 (group 32, 64 or 128), w_zeros the same shape uint8
+    (8 without), plus an optional fp32 bias [N]. swiglu: silu(first half of the
+    features) times the second half, [T][N/2]."""
+    dev = _place(x, w, w_scales, w_zeros, bias, out)
+    if w.dim() != 2:
+        raise ValueError("w must be 2-D")
+    return _w4("moe_linear_w4", dev, stream, x, (), (), w, w_scales, w_zeros, bias, swiglu,
+               out_dtype, out)
+
+
+def moe_grouped_linear_w4(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                          w_scales: torch.Tensor, w_zeros: Optional[torch.Tensor] = None,
+                          bias: Optional[torch.Tensor] = None, swiglu: bool = False,
+                          out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """moe_linear_w4 by expert: rows offsets[e] .. offsets[e+1]-1 of x (moe_dispatch's
+    order) times expert e's weight; w [E][N][K/2], w_scales and w_zeros
+    [E][N][K/group], bias [E][N]. Rows outside all experts' are left as they were."""
+    dev = _place(x, offsets, w, w_scales, w_zeros, bias, out)
+    if w.dim() != 3:
+        raise ValueError("w must be 3-D")
+    E = w.shape[0]
+    _flat(offsets, (E + 1,), torch.int32, "offsets")
+    return _w4("moe_grouped_linear_w4", dev, stream, x, (_addr(offsets),), (E,), w, w_scales,
+               w_zeros, bias, swiglu, out_dtype, out)

@@ -438,6 +438,102 @@ moe_status moe_linear_e4m3(const uint8_t* codes, const uint8_t* exps, const uint
 moe_status moe_swiglu_quantize_e4m3(const void* gate_up, int64_t ld, int64_t tokens,
                                     int32_t inter, uint8_t* codes, uint8_t* exps, void* stream);
 
+/* ---- Rows to their experts and back ----
+ * The layer's permutation and combine for experts that the caller computes:
+ * the rows of a batch sorted by expert, the experts' results weighted back, and
+ * the gradients of both (colizig page, "Features": routed experts evaluated one
+ * group at a time, the result that of the serial order).
+ * Slot t * top_k + j is the j-th choice of token t. Rows are sorted by expert,
+ * within an expert by slot. A slot whose expert is outside [0, experts), as on a
+ * device that holds a share of the experts or for a padded token, has no row and
+ * takes no part; a token may have none, and may name an expert twice (two rows).
+ *   dispatch           rows[inv[s]] = x[t]
+ *   dispatch_backward  dx[t]  = sum_j d_rows[inv[t,j]]
+ *   combine            out[t] = sum_j gates[t,j] y[inv[t,j]] (+ shared[t])
+ *   combine_backward   d_y[inv[t,j]] = gates[t,j] d_out[t]
+ *                      d_gates[t,j]  = sum_h d_out[t][h] y[inv[t,j]][h]  (0 without a row)
+ * Sums are fp32, j ascending (shared last), and rounded once. (The gradient of
+ * shared is d_out.)
+ *   x, d_rows, y, shared, rows, dx, out, d_out, d_y: matrices of `hidden` columns of
+ *            fp32 or bf16, rows ld_* elements apart (at least hidden); elements
+ *            between rows are left alone. Any hidden, distance and element-aligned
+ *            address; accesses are widest where all are multiples of 8 elements
+ *            (16 bytes)
+ *   topk_idx [tokens][top_k] int32
+ *   rows     [tokens * top_k] rows, written up to offsets[experts]; those behind
+ *            stay as they were
+ *   offsets  [experts + 1] int32: expert e's rows are offsets[e] .. offsets[e+1]-1
+ *            (written for tokens == 0, too)
+ *   pair     [tokens * top_k] int32: a row's slot, -1 behind the last row
+ *   inv      [tokens][top_k] int32: a slot's row, -1 without one. The functions
+ *            that read it take any value outside [0, rows) as no row; a row is
+ *            named by one slot at most
+ *   gates, d_gates [tokens][top_k] fp32
+ *   rows     (of the functions that read inv) the number of rows of d_rows, y and
+ *            d_y. Rows of d_y without a slot stay as they were
+ * Results overlap no input. top_k <= 16, experts <= 1024, hidden <= 2^20, tokens * top_k <=
+ * 2^27, tokens * ceil(hidden / 256) < 2^24 (else MOE_ERR_UNSUPPORTED). The
+ * workspace of moe_dispatch is moe_dispatch_workspace_bytes() (0: NULL is
+ * allowed), 256-byte aligned; calls that overlap need one each. */
+size_t moe_dispatch_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);
+moe_status moe_dispatch(const void* x, int64_t ld_x, moe_dtype dtype, const int32_t* topk_idx,
+                        int64_t tokens, int32_t hidden, int32_t top_k, int32_t experts,
+                        void* rows, int64_t ld_rows, int32_t* offsets, int32_t* pair,
+                        int32_t* inv, void* workspace, size_t workspace_bytes, void* stream);
+moe_status moe_dispatch_backward(const void* d_rows, int64_t ld_rows, int64_t rows,
+                                 moe_dtype dtype, const int32_t* inv, int64_t tokens,
+                                 int32_t hidden, int32_t top_k, void* dx, int64_t ld_dx,
+                                 moe_dtype dx_dtype, void* stream);
+moe_status moe_combine(const void* y, int64_t ld_y, int64_t rows, moe_dtype dtype,
+                       const float* gates, const int32_t* inv, const void* shared,
+                       int64_t ld_shared, int64_t tokens, int32_t hidden, int32_t top_k, void* out,
+                       int64_t ld_out, moe_dtype out_dtype, void* stream);
+moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dtype, const void* y,
+                                int64_t ld_y, int64_t rows, moe_dtype dtype, const float* gates,
+                                const int32_t* inv, int64_t tokens, int32_t hidden, int32_t top_k,
+                                void* d_y, int64_t ld_dy, float* d_gates, void* stream);
+
+/* ---- Products with 4-bit weights ----
+ *   y[t][n] = sum_k x[t][k] * W[n][k] (+ bias[n]),
+ *   W[n][k] = (q[n][k] - z[n][k/group]) * s[n][k/group]
+ * dense, or by expert for rows sorted as moe_dispatch sorts them: row t of
+ * expert e (offsets[e] <= t < offsets[e+1]) is multiplied with that expert's
+ * matrix. With swiglu = 1 the first half of the features are gates g and the
+ * second half u, and out[t][i] = silu(g_i) * u_i of out_features / 2 columns.
+ * x is multiplied as it is; sums, scales and zero points are fp32, rounded once
+ * to the output type. (zilda page, "Roadmap", and colizig page, "Status", name
+ * 4-bit weights as a coming step; the format is a reading of this project.)
+ *   x        [rows] rows of in_features bf16 values, finite, ld_x elements apart
+ *            (a multiple of 8, at least in_features), 16-byte aligned
+ *   offsets  [experts + 1] int32, ascending, on the device; values are cut to
+ *            [0, rows], and rows outside all experts' are left alone in out
+ *   w        [experts][out_features][in_features / 2] bytes, 16-byte aligned: the
+ *            code of an even column in a byte's low four bits, of the next one
+ *            in its high four
+ *   w_scales [experts][out_features][in_features / group], fp32 or bf16,
+ *            magnitudes below 2^100
+ *   w_zeros  the same shape, a byte each, or NULL: every z is 8
+ *   bias     [experts][out_features] fp32, or NULL for none
+ *   out      [rows] rows of out_features values (half with swiglu) of out_dtype,
+ *            ld_out elements apart; elements between rows are left alone. It
+ *            overlaps no input
+ * (experts: without it for moe_linear_w4.) group is 32, 64 or 128 and divides
+ * in_features; out_features is free, but even with swiglu. A row's result does not
+ * depend on the other rows' values. in_features, out_features, rows <= 2^20 and
+ * ceil(rows/16) * ceil(out_features/16) < 2^23, by expert with experts more tiles of
+ * rows (else MOE_ERR_UNSUPPORTED). rows == 0 enqueues nothing. */
+moe_status moe_linear_w4(const void* x, int64_t ld_x, const uint8_t* w, const void* w_scales,
+                         moe_dtype scale_dtype, const uint8_t* w_zeros, const float* bias,
+                         int64_t rows, int32_t out_features, int32_t in_features, int32_t group,
+                         int32_t swiglu, void* out, int64_t ld_out, moe_dtype out_dtype,
+                         void* stream);
+moe_status moe_grouped_linear_w4(const void* x, int64_t ld_x, const int32_t* offsets,
+                                 const uint8_t* w, const void* w_scales, moe_dtype scale_dtype,
+                                 const uint8_t* w_zeros, const float* bias, int64_t rows,
+                                 int32_t experts, int32_t out_features, int32_t in_features,
+                                 int32_t group, int32_t swiglu, void* out, int64_t ld_out,
+                                 moe_dtype out_dtype, void* stream);
+
 /* Intermediate results of moe_forward, readable from its workspace once the
  * call's stream work has completed (the workspace is the caller's memory).
  * moe_workspace_region reports where one of them lies for `cfg`:

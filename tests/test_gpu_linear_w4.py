@@ -1,0 +1,298 @@
+"""Products with 4-bit weights (moe_linear_w4, moe_grouped_linear_w4) against the
+formula in 64 bits, and the layer that they make with moe_dispatch and moe_combine.
+
+The bound of an element: a term x (q or z) s meets at most 64 + K / 32 fp32 roundings
+(32 inside an instruction, four instructions of a group, the group's scale and zero
+point, one addition a group or instruction after it), each 2^-24 of the magnitudes
+summed so far, which sum |x| (q + z) |s| bounds; half a step of the output type
+comes on top. SwiGLU passes the errors of gate and up on with |silu'| <= 1.1 and
+|silu|, and adds 2^-20 of its own value (exponential, quotient, two products; the
+exponential's argument has 2^-24 |g|, |g| up to 8 here)."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_dispatch import HALF, TYPES, choices, permutation
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(lead, N, K, G, seed, scales="f32", zeros=True, bias=False):
+    r = np.random.default_rng(seed)
+    w = r.integers(0, 256, (*lead, N, K // 2)).astype(np.uint8)
+    s = (np.exp2(r.uniform(-2, 2, (*lead, N, K // G))) * 0.02 * r.choice([-1, 1], (*lead, N, K // G)))
+    s = torch.from_numpy(s.astype(np.float32)).to(TYPES[scales])
+    z = torch.from_numpy(r.integers(0, 20, s.shape).astype(np.uint8)) if zeros else None
+    b = torch.from_numpy(r.normal(size=(*lead, N)).astype(np.float32)) if bias else None
+    return tuple(None if t is None else t.cuda() for t in (torch.from_numpy(w), s, z, b))
+
+
+def activations(M, K, seed, pad=0):
+    r = np.random.default_rng(seed)
+    x = r.normal(size=(M, K + pad)).astype(np.float32)
+    x[:, r.random(K + pad) < 0.02] *= 12
+    return torch.from_numpy(x).to(torch.bfloat16).cuda()[:, :K]
+
+
+def values(w, s, z):
+    """(W, |q + z| |s|) of [n][k/2] codes in 64 bits."""
+    w, s = w.cpu().numpy(), s.double().cpu().numpy()
+    z = np.full(s.shape, 8.0) if z is None else z.cpu().numpy().astype(np.float64)
+    n, half = w.shape
+    q = np.empty((n, 2 * half))
+    q[:, 0::2], q[:, 1::2] = w & 15, w >> 4
+    G = 2 * half // s.shape[1]
+    s, z = np.repeat(s, G, axis=1), np.repeat(z, G, axis=1)
+    return (q - z) * s, (q + z) * np.abs(s)
+
+
+def reference(x, w, s, z, b, swiglu):
+    """(out, bound of fp32 errors) in 64 bits."""
+    x = x.double().cpu().numpy()
+    v, mag = values(w, s, z)
+    y = x @ v.T
+    err = (64 + x.shape[1] / 32) * 2.0 ** -24 * (np.abs(x) @ mag.T)
+    if b is not None:
+        b = b.double().cpu().numpy()
+        y, err = y + b, err + 2.0 ** -24 * (np.abs(y) + np.abs(b))
+    if swiglu:
+        i = y.shape[1] // 2
+        g, u, eg, eu = y[:, :i], y[:, i:], err[:, :i], err[:, i:]
+        e = np.exp(-np.abs(g))
+        silu = g * np.where(g >= 0, 1 / (1 + e), e / (1 + e))
+        y = silu * u
+        err = 1.1 * eg * (np.abs(u) + eu) + np.abs(silu) * eu + 2.0 ** -20 * np.abs(y)
+    return y, err
+
+
+def check(got, ref, err, what=""):
+    got64 = got.double().cpu().numpy()
+    off = np.abs(got64 - ref)
+    lim = err + HALF[got.dtype] * (np.abs(ref) + err) + 1e-45
+    assert np.isfinite(got64).all(), what
+    assert (off <= lim).all(), f"{what}: {np.max(off / lim):.2f} of the bound"
+
+
+ROWS = [1, 2, 15, 16, 17, 33, 64, 65, 130, 300]
+
+
+@pytest.mark.parametrize("M", ROWS)
+@pytest.mark.parametrize("G,N,K", [(128, 96, 1024), (64, 35, 448), (32, 130, 352), (32, 1, 32),
+                                   (64, 200, 64), (128, 64, 128)])
+def test_product(M, G, N, K):
+    import block_fp8_routed_amd as moe
+    for i, (scales, zeros, bias, out) in enumerate([("f32", True, True, "f32"),
+                                                    ("bf16", False, False, "bf16")]):
+        w, s, z, b = weights((), N, K, G, M + i, scales, zeros, bias)
+        x = activations(M, K, M)
+        got = moe.moe_linear_w4(x, w, s, z, bias=b, out_dtype=TYPES[out])
+        check(got, *reference(x, w, s, z, b, False), f"{scales} {out}")
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 129, 520])
+@pytest.mark.parametrize("G,N,K", [(128, 1536, 2048), (64, 258, 320), (32, 2, 96), (32, 130, 128)])
+def test_swiglu(M, G, N, K):
+    import block_fp8_routed_amd as moe
+    w, s, z, b = weights((), N, K, G, M, "bf16", M % 2 == 0, True)
+    x = activations(M, K, M)
+    for out in TYPES.values():
+        got = moe.moe_linear_w4(x, w, s * 0.05, z, bias=b, swiglu=True, out_dtype=out)
+        assert got.shape == (M, N // 2)
+        check(got, *reference(x, w, s * 0.05, z, b, True), str(out))
+
+
+@pytest.mark.parametrize("M,N,K,G", [(1, 4096, 4096, 128), (16, 512, 8192, 64), (77, 2112, 4096, 32),
+                                     (1000, 640, 1024, 128), (2049, 300, 512, 64)])
+def test_long_and_wide_products(M, N, K, G):
+    import block_fp8_routed_amd as moe
+    w, s, z, _ = weights((), N, K, G, 3, "f32", True)
+    x = activations(M, K, 4)
+    got = moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32)
+    check(got, *reference(x, w, s, z, None, False))
+
+
+def test_every_code_and_zero_point():
+    """One column set at a time: out is exactly (q - z) s x for every q and z."""
+    import block_fp8_routed_amd as moe
+    K, N = 128, 256 * 16
+    q, z = np.meshgrid(np.arange(16), np.arange(256))
+    codes = (q.reshape(-1) | q.reshape(-1) << 4).astype(np.uint8)
+    w = torch.from_numpy(np.repeat(codes[:, None], K // 2, axis=1)).cuda()
+    zero = torch.from_numpy(np.repeat(z.reshape(-1, 1), 4, axis=1).astype(np.uint8)).cuda()
+    s = torch.full((N, 4), 0.5, device="cuda")
+    for M in (1, 128):
+        x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+        x[torch.arange(M), torch.arange(M) % K] = 2.0
+        got = moe.moe_linear_w4(x, w, s, zero, out_dtype=torch.float32)
+        want = torch.from_numpy((q - z).reshape(-1).astype(np.float32)).cuda().expand(M, N)
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [1, 20, 200])
+def test_columns_meet_their_codes(M):
+    """x = a unit vector picks one column of W: exact."""
+    import block_fp8_routed_amd as moe
+    N, K, G = 48, 416, 32
+    w, s, z, _ = weights((), N, K, G, 5)
+    v, _ = values(w, s, z)
+    for k0 in range(0, K, M):
+        x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+        n = min(M, K - k0)
+        x[torch.arange(n), k0 + torch.arange(n)] = 1.0
+        got = moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32)[:n]
+        assert np.array_equal(got.cpu().numpy(), v[:, k0:k0 + n].T.astype(np.float32))
+
+
+@pytest.mark.parametrize("M", [3, 100])
+def test_strided_rows_and_outputs(M):
+    import block_fp8_routed_amd as moe
+    N, K, G = 70, 256, 64
+    w, s, z, _ = weights((), N, K, G, 6)
+    x = activations(M, K, 7, pad=24)
+    for out in TYPES.values():
+        for pad in (2, 7):
+            whole = torch.full((M, N + pad), 4.0, dtype=out, device="cuda")
+            got = moe.moe_linear_w4(x, w, s, z, out=whole[:, 1:N + 1])
+            check(got, *reference(x, w, s, z, None, False))
+            assert bool((whole[:, 0] == 4).all()) and bool((whole[:, N + 1:] == 4).all())
+
+
+@pytest.mark.parametrize("M", [16, 64, 200])
+def test_a_row_of_nan_stays_in_its_row(M):
+    import block_fp8_routed_amd as moe
+    w, s, z, _ = weights((), 50, 256, 64, 8)
+    x = activations(M, 256, 9)
+    want = moe.moe_linear_w4(x, w, s, z)
+    x[5] = float("nan")
+    x[7, 3] = float("inf")
+    got = moe.moe_linear_w4(x, w, s, z)
+    rest = torch.ones(M, dtype=torch.bool)
+    rest[[5, 7]] = False
+    assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[5]).all())
+    assert not bool(torch.isfinite(got[7]).any())
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 100, 2.0 ** -118])
+def test_ends_of_the_range(scale):
+    """Large and small rows, their sums and the scales' products within fp32's range."""
+    import block_fp8_routed_amd as moe
+    w, s, z, _ = weights((), 40, 256, 128, 10)
+    for M in (2, 90):
+        x = (activations(M, 256, 11).float() * scale).to(torch.bfloat16)
+        ref, err = reference(x, w, s, z, None, False)
+        # below 2^-126 fp32 keeps steps of 2^-149, one for each of the roundings
+        err = err + (64 + 256 / 32) * 2.0 ** -149 * 256 * 512
+        check(moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32), ref, err)
+
+
+def grouped_reference(x, offsets, w, s, z, b, swiglu):
+    n = w.shape[1] // 2 if swiglu else w.shape[1]
+    ref, err = np.zeros((x.shape[0], n)), np.zeros((x.shape[0], n))
+    for e in range(w.shape[0]):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if lo < hi:
+            one = [None if t is None else t[e] for t in (w, s, z, b)]
+            ref[lo:hi], err[lo:hi] = reference(x[lo:hi], *one, swiglu)
+    return ref, err
+
+
+COUNTS = {
+    "one_row": [0, 0, 1, 0], "even": [5, 5, 5, 5], "uneven": [0, 300, 1, 0, 17, 16, 0, 64, 129, 0],
+    "single": [140], "none": [0, 0, 0], "last": [0] * 99 + [33], "many": [1, 0, 2] * 230,
+    "tiles": [32, 64, 128, 256, 31, 33, 63, 65],
+}
+
+
+@pytest.mark.parametrize("name", list(COUNTS))
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("G", [32, 128])
+def test_grouped(name, swiglu, G):
+    import block_fp8_routed_amd as moe
+    counts = COUNTS[name]
+    E, N, K = len(counts), 72, 256
+    offsets = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
+    behind = 7  # rows of no expert
+    M = int(offsets[-1]) + behind
+    w, s, z, b = weights((E,), N, K, G, 12, "bf16" if G == 32 else "f32", swiglu, True)
+    s = s * 0.1
+    x = activations(M, K, 13)
+    n = N // 2 if swiglu else N
+    out = torch.full((M, n), 6.0, dtype=torch.bfloat16 if swiglu else torch.float32, device="cuda")
+    got = moe.moe_grouped_linear_w4(x, torch.from_numpy(offsets).cuda(), w, s, z, bias=b,
+                                    swiglu=swiglu, out=out)
+    ref, err = grouped_reference(x, offsets, w, s, z, b, swiglu)
+    check(got[:M - behind], ref[:M - behind], err[:M - behind])
+    assert bool((out[M - behind:] == 6).all())
+
+
+def test_offsets_are_cut_to_the_rows():
+    """Offsets beyond the rows, negative or falling name no row outside x and out."""
+    import block_fp8_routed_amd as moe
+    M, N, K = 40, 32, 128
+    w, s, z, _ = weights((4,), N, K, 128, 14)
+    x = activations(M, K, 15)
+    out = torch.full((M, N), 6.0, dtype=torch.float32, device="cuda")
+    offsets = torch.tensor([-5, 10, 4, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32).cuda()
+    moe.moe_grouped_linear_w4(x, offsets, w, s, z, out=out)
+    # expert 0: rows 0 .. 9, expert 1: none, expert 2: 4 .. 39 (over 4 .. 9), expert 3: none
+    ref, err = reference(x, w[2], s[2], z[2], None, False)
+    check(out[10:], ref[10:], err[10:])
+    ref, err = reference(x, w[0], s[0], z[0], None, False)
+    check(out[:4], ref[:4], err[:4])
+
+
+def test_a_row_does_not_depend_on_the_batch_of_one_kernel():
+    """Rows of a batch of one size keep their bits whatever the other rows hold."""
+    import block_fp8_routed_amd as moe
+    w, s, z, _ = weights((), 100, 512, 64, 16)
+    for M in (16, 100, 600):
+        x = activations(M, 512, 17)
+        a = moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32)
+        y = x.clone()
+        y[M // 2:] = activations(M - M // 2, 512, 18) * 100
+        b = moe.moe_linear_w4(y, w, s, z, out_dtype=torch.float32)
+        assert torch.equal(a[:M // 2], b[:M // 2])
+        assert torch.equal(b, moe.moe_linear_w4(y, w, s, z, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 512, 10, 256, 128), (16, 128, 8, 512, 192), (300, 8, 2, 256, 160)])
+@pytest.mark.parametrize("share", [False, True])
+def test_layer_of_4_bit_experts(T, E, k, H, I, share):
+    """dispatch, gate/up with SwiGLU, down, combine, as they are used together; and
+    captured, replayed with other inputs beside eager work."""
+    import block_fp8_routed_amd as moe
+    w1, s1, z1, _ = weights((E,), 2 * I, H, 32, 1, "bf16", True)
+    w2, s2, z2, _ = weights((E,), H, I, 32, 2, "bf16", False)
+    s1, s2 = s1 * 0.2, s2 * 0.2
+    x = activations(T, H, 3)
+    idx = torch.from_numpy(choices(T, k, E, 4, "share" if share else "distinct")).cuda()
+    gates = torch.rand(T, k, device="cuda")
+
+    def layer():
+        rows, offsets, _, inv = moe.moe_dispatch(x, idx, E)
+        h = moe.moe_grouped_linear_w4(rows, offsets, w1, s1, z1, swiglu=True)
+        y = moe.moe_grouped_linear_w4(h, offsets, w2, s2, z2)
+        return h, y, moe.moe_combine(y, gates, inv, out_dtype=torch.float32)
+
+    h, y, out = layer()
+    offsets, pair, inv = permutation(idx.cpu().numpy(), E)
+    n = int(offsets[-1])
+    rows = x[torch.from_numpy(np.maximum(pair, 0).astype(np.int64) // k).cuda()]
+    check(h[:n], *(t[:n] for t in grouped_reference(rows, offsets, w1, s1, z1, None, True)))
+    # each later step on what the kernels before it gave
+    check(y[:n], *(t[:n] for t in grouped_reference(h, offsets, w2, s2, z2, None, False)))
+    v = np.where((inv >= 0)[:, :, None], y.double().cpu().numpy()[np.maximum(inv, 0)], 0.0)
+    v = v * gates.double().cpu().numpy()[:, :, None]
+    check(out, v.sum(axis=1), k * 2.0 ** -24 * np.abs(v).sum(axis=1))
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = layer()[2]
+    for seed in range(3):
+        x.copy_(activations(T, H, 20 + seed))
+        idx.copy_(torch.from_numpy(choices(T, k, E, 30 + seed, "share" if share else "any")))
+        want = layer()[2]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, want)
