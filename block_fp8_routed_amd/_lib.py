@@ -34,7 +34,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_forward", "moe_forward_static", "moe_forw
            "moe_linear_workspace_bytes", "moe_linear", "moe_linear_e4m3",
            "moe_swiglu_quantize_e4m3",
            "moe_dispatch_workspace_bytes", "moe_dispatch", "moe_dispatch_backward",
-           "moe_combine", "moe_combine_backward", "moe_linear_w4", "moe_grouped_linear_w4",
+           "moe_combine", "moe_combine_backward", "moe_linear_w4_workspace_bytes",
+           "moe_linear_w4", "moe_grouped_linear_w4",
            "moe_status_string", "moe_version", "moe_set_wait_limit")
 (MOE_WS_TOPK, MOE_WS_GATES, MOE_WS_OFFSETS, MOE_WS_PAIR, MOE_WS_INV, MOE_WS_H, MOE_WS_H_EXPS,
  MOE_WS_Y, MOE_WS_Y_EXPS, MOE_WS_STATUS, MOE_WS_COUNT) = range(11)
@@ -154,9 +155,12 @@ def load() -> ctypes.CDLL:
     lib.moe_combine.argtypes = [P, I64, I64, INT, P, P, P, I64, I64, I32, I32, P, I64, INT, P]
     lib.moe_combine_backward.argtypes = [P, I64, INT, P, I64, I64, INT, P, P, I64, I32, I32, P,
                                          I64, P, P]
-    lib.moe_linear_w4.argtypes = [P, I64, P, P, INT, P, P, I64, I32, I32, I32, I32, P, I64, INT, P]
+    lib.moe_linear_w4_workspace_bytes.argtypes = [I64, I32, I32, INT]
+    lib.moe_linear_w4_workspace_bytes.restype = SZ
+    lib.moe_linear_w4.argtypes = [P, I64, P, P, INT, P, P, I64, I32, I32, I32, I32, P, I64, INT, P,
+                                  SZ, P]
     lib.moe_grouped_linear_w4.argtypes = [P, I64, P, P, P, INT, P, P, I64, I32, I32, I32, I32, I32,
-                                          P, I64, INT, P]
+                                          P, I64, INT, P, SZ, P]
     for name in ("moe_select_experts", "moe_route_gated", "moe_forward_gated", "moe_linear",
                  "moe_linear_e4m3", "moe_swiglu_quantize_e4m3", "moe_dispatch",
                  "moe_dispatch_backward", "moe_combine", "moe_combine_backward", "moe_linear_w4",
@@ -885,7 +889,14 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, gates: torch.Tens
     return d_y, d_gates
 
 
-def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, out_dtype, out):
+@functools.lru_cache(maxsize=1024)
+def linear_w4_workspace_bytes(rows: int, experts: int, in_features: int, out_dtype: int) -> int:
+    """moe_linear_w4_workspace_bytes (a function of the sizes and moe_dtype alone)."""
+    return int(load().moe_linear_w4_workspace_bytes(rows, experts, in_features, out_dtype))
+
+
+def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, out_dtype, out,
+        workspace):
     """The checks and the call that both 4-bit products share; lead: () or (experts,)."""
     if x.dim() != 2 or x.dtype != torch.bfloat16:
         raise ValueError("x must be a 2-D bfloat16 tensor")
@@ -901,40 +912,45 @@ def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, ou
     _flat(w_zeros, (*lead, N, groups), torch.uint8, "w_zeros")
     _flat(bias, (*lead, N), torch.float32, "bias")
     res, code, ld_out = _result(out, x, M, N // 2 if swiglu else N, out_dtype, stream)
+    if workspace is None:
+        need = linear_w4_workspace_bytes(M, lead[0] if lead else 1, K, code)
+        if need:
+            workspace = _empty(x, (need,), torch.uint8, stream)
     _enqueue(getattr(_lib or load(), name), name, dev, stream, _addr(x), ld, *head, _addr(w),
              _addr(w_scales), scale, _addr(w_zeros), _addr(bias), M, *lead, N, K, K // groups,
-             bool(swiglu), _addr(res), ld_out, code)
+             bool(swiglu), _addr(res), ld_out, code, _addr(workspace), _bytes(workspace))
     return res
 
 
 def moe_linear_w4(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
                   w_zeros: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
                   swiglu: bool = False, out_dtype=torch.bfloat16,
-                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
     """x [T][K] bf16 (rows may lie apart) times the transpose of a 4-bit weight
     (q - z) s: w [N][K/2] uint8 (the even column in the low four bits), w_scales
     [N][K/group] fp32 or bf16 (group 32, 64 or 128), w_zeros the same shape uint8
     (8 without), plus an optional fp32 bias [N]. swiglu: silu(first half of the
     features) times the second half, [T][N/2]."""
-    dev = _place(x, w, w_scales, w_zeros, bias, out)
+    dev = _place(x, w, w_scales, w_zeros, bias, out, workspace)
     if w.dim() != 2:
         raise ValueError("w must be 2-D")
     return _w4("moe_linear_w4", dev, stream, x, (), (), w, w_scales, w_zeros, bias, swiglu,
-               out_dtype, out)
+               out_dtype, out, workspace)
 
 
 def moe_grouped_linear_w4(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
                           w_scales: torch.Tensor, w_zeros: Optional[torch.Tensor] = None,
                           bias: Optional[torch.Tensor] = None, swiglu: bool = False,
                           out_dtype=torch.bfloat16, out: Optional[torch.Tensor] = None,
-                          stream=None) -> torch.Tensor:
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_linear_w4 by expert: rows offsets[e] .. offsets[e+1]-1 of x (moe_dispatch's
     order) times expert e's weight; w [E][N][K/2], w_scales and w_zeros
     [E][N][K/group], bias [E][N]. Rows outside all experts' are left as they were."""
-    dev = _place(x, offsets, w, w_scales, w_zeros, bias, out)
+    dev = _place(x, offsets, w, w_scales, w_zeros, bias, out, workspace)
     if w.dim() != 3:
         raise ValueError("w must be 3-D")
     E = w.shape[0]
     _flat(offsets, (E + 1,), torch.int32, "offsets")
     return _w4("moe_grouped_linear_w4", dev, stream, x, (_addr(offsets),), (E,), w, w_scales,
-               w_zeros, bias, swiglu, out_dtype, out)
+               w_zeros, bias, swiglu, out_dtype, out, workspace)

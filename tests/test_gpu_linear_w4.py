@@ -7,7 +7,13 @@ point, one addition a group or instruction after it), each 2^-24 of the magnitud
 summed so far, which sum |x| (q + z) |s| bounds; half a step of the output type
 comes on top. SwiGLU passes the errors of gate and up on with |silu'| <= 1.1 and
 |silu|, and adds 2^-20 of its own value (exponential, quotient, two products; the
-exponential's argument has 2^-24 |g|, |g| up to 8 here)."""
+exponential's argument has 2^-24 |g|, |g| up to 8 here).
+
+bf16 output of larger batches multiplies fp16 weights: scale and product are rounded
+once each, half a step of fp16's 11 bits, 2^-11, each time: 2^-10 + 2^-22 of a term; where
+they fall below fp16's normal numbers, by 2^-25 each, the scale's times |q - z| <
+2^8, where the row's largest scale is at least 2^6: 2^-22 of that scale for both
+and every |x|. A row of x keeps 2^-40 of its largest magnitude. `half` adds these."""
 import numpy as np
 import pytest
 import torch
@@ -46,12 +52,17 @@ def values(w, s, z):
     return (q - z) * s, (q + z) * np.abs(s)
 
 
-def reference(x, w, s, z, b, swiglu):
-    """(out, bound of fp32 errors) in 64 bits."""
+def reference(x, w, s, z, b, swiglu, half=True):
+    """(out, bound of the errors before its rounding) in 64 bits."""
     x = x.double().cpu().numpy()
     v, mag = values(w, s, z)
     y = x @ v.T
     err = (64 + x.shape[1] / 32) * 2.0 ** -24 * (np.abs(x) @ mag.T)
+    if half:
+        a = np.abs(x)
+        smax = s.double().abs().amax(dim=1).cpu().numpy()
+        err = (err + (2.0 ** -10 + 2.0 ** -22) * (a @ np.abs(v).T) + 2.0 ** -22 * a.sum(axis=1)[:, None] * smax
+               + 2.0 ** -40 * a.max(axis=1)[:, None] * np.abs(v).sum(axis=1))
     if b is not None:
         b = b.double().cpu().numpy()
         y, err = y + b, err + 2.0 ** -24 * (np.abs(y) + np.abs(b))
@@ -86,7 +97,7 @@ def test_product(M, G, N, K):
         w, s, z, b = weights((), N, K, G, M + i, scales, zeros, bias)
         x = activations(M, K, M)
         got = moe.moe_linear_w4(x, w, s, z, bias=b, out_dtype=TYPES[out])
-        check(got, *reference(x, w, s, z, b, False), f"{scales} {out}")
+        check(got, *reference(x, w, s, z, b, False, out == "bf16"), f"{scales} {out}")
 
 
 @pytest.mark.parametrize("M", [1, 16, 40, 129, 520])
@@ -98,7 +109,7 @@ def test_swiglu(M, G, N, K):
     for out in TYPES.values():
         got = moe.moe_linear_w4(x, w, s * 0.05, z, bias=b, swiglu=True, out_dtype=out)
         assert got.shape == (M, N // 2)
-        check(got, *reference(x, w, s * 0.05, z, b, True), str(out))
+        check(got, *reference(x, w, s * 0.05, z, b, True, out == torch.bfloat16), str(out))
 
 
 @pytest.mark.parametrize("M,N,K,G", [(1, 4096, 4096, 128), (16, 512, 8192, 64), (77, 2112, 4096, 32),
@@ -107,8 +118,9 @@ def test_long_and_wide_products(M, N, K, G):
     import block_fp8_routed_amd as moe
     w, s, z, _ = weights((), N, K, G, 3, "f32", True)
     x = activations(M, K, 4)
-    got = moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32)
-    check(got, *reference(x, w, s, z, None, False))
+    for out in TYPES.values():
+        got = moe.moe_linear_w4(x, w, s, z, out_dtype=out)
+        check(got, *reference(x, w, s, z, None, False, out == torch.bfloat16), str(out))
 
 
 def test_every_code_and_zero_point():
@@ -123,9 +135,9 @@ def test_every_code_and_zero_point():
     for M in (1, 128):
         x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
         x[torch.arange(M), torch.arange(M) % K] = 2.0
-        got = moe.moe_linear_w4(x, w, s, zero, out_dtype=torch.float32)
         want = torch.from_numpy((q - z).reshape(-1).astype(np.float32)).cuda().expand(M, N)
-        assert torch.equal(got, want)
+        for out in TYPES.values():
+            assert torch.equal(moe.moe_linear_w4(x, w, s, zero, out_dtype=out), want.to(out))
 
 
 @pytest.mark.parametrize("M", [1, 20, 200])
@@ -141,6 +153,11 @@ def test_columns_meet_their_codes(M):
         x[torch.arange(n), k0 + torch.arange(n)] = 1.0
         got = moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32)[:n]
         assert np.array_equal(got.cpu().numpy(), v[:, k0:k0 + n].T.astype(np.float32))
+        got = moe.moe_linear_w4(x, w, s, z)[:n].double().cpu().numpy()
+        want = v[:, k0:k0 + n].T
+        # two roundings to fp16 (half a step of its 11 bits is 2^-11) and one to bf16
+        # (2^-8): (1 + 2^-11)^2 (1 + 2^-8) - 1 < 2^-8 + 2^-10 + 2^-17
+        assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -17) * np.abs(want)).all()
 
 
 @pytest.mark.parametrize("M", [3, 100])
@@ -153,7 +170,7 @@ def test_strided_rows_and_outputs(M):
         for pad in (2, 7):
             whole = torch.full((M, N + pad), 4.0, dtype=out, device="cuda")
             got = moe.moe_linear_w4(x, w, s, z, out=whole[:, 1:N + 1])
-            check(got, *reference(x, w, s, z, None, False))
+            check(got, *reference(x, w, s, z, None, False, out == torch.bfloat16))
             assert bool((whole[:, 0] == 4).all()) and bool((whole[:, N + 1:] == 4).all())
 
 
@@ -179,20 +196,20 @@ def test_ends_of_the_range(scale):
     w, s, z, _ = weights((), 40, 256, 128, 10)
     for M in (2, 90):
         x = (activations(M, 256, 11).float() * scale).to(torch.bfloat16)
-        ref, err = reference(x, w, s, z, None, False)
+        ref, err = reference(x, w, s, z, None, False, False)
         # below 2^-126 fp32 keeps steps of 2^-149, one for each of the roundings
         err = err + (64 + 256 / 32) * 2.0 ** -149 * 256 * 512
         check(moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32), ref, err)
 
 
-def grouped_reference(x, offsets, w, s, z, b, swiglu):
+def grouped_reference(x, offsets, w, s, z, b, swiglu, half=True):
     n = w.shape[1] // 2 if swiglu else w.shape[1]
     ref, err = np.zeros((x.shape[0], n)), np.zeros((x.shape[0], n))
     for e in range(w.shape[0]):
         lo, hi = int(offsets[e]), int(offsets[e + 1])
         if lo < hi:
             one = [None if t is None else t[e] for t in (w, s, z, b)]
-            ref[lo:hi], err[lo:hi] = reference(x[lo:hi], *one, swiglu)
+            ref[lo:hi], err[lo:hi] = reference(x[lo:hi], *one, swiglu, half)
     return ref, err
 
 
@@ -220,7 +237,7 @@ def test_grouped(name, swiglu, G):
     out = torch.full((M, n), 6.0, dtype=torch.bfloat16 if swiglu else torch.float32, device="cuda")
     got = moe.moe_grouped_linear_w4(x, torch.from_numpy(offsets).cuda(), w, s, z, bias=b,
                                     swiglu=swiglu, out=out)
-    ref, err = grouped_reference(x, offsets, w, s, z, b, swiglu)
+    ref, err = grouped_reference(x, offsets, w, s, z, b, swiglu, swiglu)
     check(got[:M - behind], ref[:M - behind], err[:M - behind])
     assert bool((out[M - behind:] == 6).all())
 
@@ -235,9 +252,9 @@ def test_offsets_are_cut_to_the_rows():
     offsets = torch.tensor([-5, 10, 4, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32).cuda()
     moe.moe_grouped_linear_w4(x, offsets, w, s, z, out=out)
     # expert 0: rows 0 .. 9, expert 1: none, expert 2: 4 .. 39 (over 4 .. 9), expert 3: none
-    ref, err = reference(x, w[2], s[2], z[2], None, False)
+    ref, err = reference(x, w[2], s[2], z[2], None, False, False)
     check(out[10:], ref[10:], err[10:])
-    ref, err = reference(x, w[0], s[0], z[0], None, False)
+    ref, err = reference(x, w[0], s[0], z[0], None, False, False)
     check(out[:4], ref[:4], err[:4])
 
 
@@ -247,12 +264,13 @@ def test_a_row_does_not_depend_on_the_batch_of_one_kernel():
     w, s, z, _ = weights((), 100, 512, 64, 16)
     for M in (16, 100, 600):
         x = activations(M, 512, 17)
-        a = moe.moe_linear_w4(x, w, s, z, out_dtype=torch.float32)
         y = x.clone()
         y[M // 2:] = activations(M - M // 2, 512, 18) * 100
-        b = moe.moe_linear_w4(y, w, s, z, out_dtype=torch.float32)
-        assert torch.equal(a[:M // 2], b[:M // 2])
-        assert torch.equal(b, moe.moe_linear_w4(y, w, s, z, out_dtype=torch.float32))
+        for out in TYPES.values():
+            a = moe.moe_linear_w4(x, w, s, z, out_dtype=out)
+            b = moe.moe_linear_w4(y, w, s, z, out_dtype=out)
+            assert torch.equal(a[:M // 2], b[:M // 2])
+            assert torch.equal(b, moe.moe_linear_w4(y, w, s, z, out_dtype=out))
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 512, 10, 256, 128), (16, 128, 8, 512, 192), (300, 8, 2, 256, 160)])

@@ -36,15 +36,16 @@ def combine_backward(d_out=P, ld_d=64, d_dtype=0, y=P, ld_y=64, rows=8, dtype=1,
 
 
 def w4(x=P, ld_x=256, w=P, ws=P, st=0, wz=None, bias=None, rows=0, n=64, k=256, group=64, swiglu=0,
-       out=P, ld_out=64, out_dtype=1):
+       out=P, ld_out=64, out_dtype=1, work=None, work_bytes=0):
     return moe.load().moe_linear_w4(x, ld_x, w, ws, st, wz, bias, rows, n, k, group, swiglu, out,
-                                    ld_out, out_dtype, None)
+                                    ld_out, out_dtype, work, work_bytes, None)
 
 
 def grouped(x=P, ld_x=256, offsets=P, w=P, ws=P, st=0, wz=None, bias=None, rows=0, experts=4, n=64,
-            k=256, group=64, swiglu=0, out=P, ld_out=64, out_dtype=1):
+            k=256, group=64, swiglu=0, out=P, ld_out=64, out_dtype=1, work=None, work_bytes=0):
     return moe.load().moe_grouped_linear_w4(x, ld_x, offsets, w, ws, st, wz, bias, rows, experts, n,
-                                            k, group, swiglu, out, ld_out, out_dtype, None)
+                                            k, group, swiglu, out, ld_out, out_dtype, work,
+                                            work_bytes, None)
 
 
 def test_no_rows_enqueue_nothing():
@@ -122,9 +123,20 @@ def test_dispatch_workspace():
     (dict(rows=4, x=P + 8), UNSUPPORTED), (dict(rows=4, w=P + 8), UNSUPPORTED),
     (dict(rows=4, ld_x=260), UNSUPPORTED), (dict(rows=4, ws=P + 2), UNSUPPORTED),
     (dict(rows=4, ws=P + 1, st=1), UNSUPPORTED), (dict(rows=4, bias=P + 2), UNSUPPORTED),
-    (dict(rows=4, out=P + 1), UNSUPPORTED), (dict(rows=4, out=P + 2, out_dtype=0), UNSUPPORTED)])
+    (dict(rows=4, out=P + 1), UNSUPPORTED), (dict(rows=4, out=P + 2, out_dtype=0), UNSUPPORTED),
+    (dict(rows=5000), NULL), (dict(rows=5000, work=P, work_bytes=1000), WORKSPACE),
+    (dict(rows=5000, work=P + 16, work_bytes=1 << 30), WORKSPACE)])
 def test_refusals_of_the_products(f, kw, status):
     assert f(**kw) == status
+
+
+def test_product_workspace():
+    assert moe.linear_w4_workspace_bytes(1, 1, 4096, moe.MOE_BF16) == 0
+    n = moe.linear_w4_workspace_bytes(5000, 1, 4000, moe.MOE_BF16)
+    assert n >= 5000 * 4000 * 2 and n % 256 == 0
+    for bad in ((-1, 1, 256, 1), (0, 1, 256, 1), (5000, 0, 256, 1), (5000, 1025, 256, 1),
+                (5000, 1, 0, 1), (1 << 21, 1, 256, 1), (5000, 1, 1 << 21, 1)):
+        assert moe.linear_w4_workspace_bytes(*bad) == 0
 
 
 def test_refusals_of_the_grouped_product():
