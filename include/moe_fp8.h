@@ -522,8 +522,7 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  * depend on the other rows' values. in_features, out_features, rows <= 2^20 and
  * ceil(rows/16) * ceil(out_features/16) < 2^23, by expert with experts more tiles of
  * rows (else MOE_ERR_UNSUPPORTED). rows == 0 enqueues nothing. */
-size_t moe_linear_w4_workspace_bytes(int64_t rows, int32_t experts, int32_t in_features,
-                                     moe_dtype out_dtype);
+size_t moe_linear_w4_workspace_bytes(int64_t rows, int32_t experts, int32_t in_features);
 moe_status moe_linear_w4(const void* x, int64_t ld_x, const uint8_t* w, const void* w_scales,
                          moe_dtype scale_dtype, const uint8_t* w_zeros, const float* bias,
                          int64_t rows, int32_t out_features, int32_t in_features, int32_t group,

@@ -9,11 +9,14 @@ comes on top. SwiGLU passes the errors of gate and up on with |silu'| <= 1.1 and
 |silu|, and adds 2^-20 of its own value (exponential, quotient, two products; the
 exponential's argument has 2^-24 |g|, |g| up to 8 here).
 
-bf16 output of larger batches multiplies fp16 weights: scale and product are rounded
-once each, half a step of fp16's 11 bits, 2^-11, each time: 2^-10 + 2^-22 of a term; where
-they fall below fp16's normal numbers, by 2^-25 each, the scale's times |q - z| <
-2^8, where the row's largest scale is at least 2^6: 2^-22 of that scale for both
-and every |x|. A row of x keeps 2^-40 of its largest magnitude. `half` adds these."""
+bf16 output of larger batches multiplies fp16 weights q S 2^-24 - z s, S = 2^24 s:
+half a step of fp16's 11 bits is 2^-11 of a value. S is rounded once, which moves
+(q - z) s by 2^-11 of itself; z s once, 2^-11 z s; the result once, 2^-11 of it. Below
+fp16's normal numbers z s and the result are off by up to 2^-25 instead, where the
+row's largest s is at least 2^-10: 2^-14 of that scale, for every |x|. `half` adds these (and 2^-20 of the first for
+their products). Both forms of the larger batches hold a row of x as fp16 times a power
+of two that brings its largest magnitude to 2^14 at least: a small value is off by up
+to 2^-25, 2^-39 or less of that magnitude, half of it where it rounds to nearest."""
 import numpy as np
 import pytest
 import torch
@@ -41,7 +44,7 @@ def activations(M, K, seed, pad=0):
 
 
 def values(w, s, z):
-    """(W, |q + z| |s|) of [n][k/2] codes in 64 bits."""
+    """(W, (q + z) |s|, z |s|) of [n][k/2] codes in 64 bits."""
     w, s = w.cpu().numpy(), s.double().cpu().numpy()
     z = np.full(s.shape, 8.0) if z is None else z.cpu().numpy().astype(np.float64)
     n, half = w.shape
@@ -49,20 +52,21 @@ def values(w, s, z):
     q[:, 0::2], q[:, 1::2] = w & 15, w >> 4
     G = 2 * half // s.shape[1]
     s, z = np.repeat(s, G, axis=1), np.repeat(z, G, axis=1)
-    return (q - z) * s, (q + z) * np.abs(s)
+    return (q - z) * s, (q + z) * np.abs(s), z * np.abs(s)
 
 
 def reference(x, w, s, z, b, swiglu, half=True):
     """(out, bound of the errors before its rounding) in 64 bits."""
     x = x.double().cpu().numpy()
-    v, mag = values(w, s, z)
+    v, mag, zero = values(w, s, z)
     y = x @ v.T
-    err = (64 + x.shape[1] / 32) * 2.0 ** -24 * (np.abs(x) @ mag.T)
+    a = np.abs(x)
+    err = ((64 + x.shape[1] / 32) * 2.0 ** -24 * (a @ mag.T)
+           + 2.0 ** -40 * a.max(axis=1)[:, None] * np.abs(v).sum(axis=1))
     if half:
-        a = np.abs(x)
         smax = s.double().abs().amax(dim=1).cpu().numpy()
-        err = (err + (2.0 ** -10 + 2.0 ** -22) * (a @ np.abs(v).T) + 2.0 ** -22 * a.sum(axis=1)[:, None] * smax
-               + 2.0 ** -40 * a.max(axis=1)[:, None] * np.abs(v).sum(axis=1))
+        err = (err + (1 + 2.0 ** -20) * (a @ (2.0 ** -10 * np.abs(v) + 2.0 ** -11 * zero).T)
+               + 2.0 ** -14 * a.sum(axis=1)[:, None] * smax)
     if b is not None:
         b = b.double().cpu().numpy()
         y, err = y + b, err + 2.0 ** -24 * (np.abs(y) + np.abs(b))
@@ -84,7 +88,7 @@ def check(got, ref, err, what=""):
     assert (off <= lim).all(), f"{what}: {np.max(off / lim):.2f} of the bound"
 
 
-ROWS = [1, 2, 15, 16, 17, 33, 64, 65, 130, 300]
+ROWS = [1, 2, 15, 16, 17, 33, 64, 65, 130, 193, 300]
 
 
 @pytest.mark.parametrize("M", ROWS)
@@ -100,7 +104,7 @@ def test_product(M, G, N, K):
         check(got, *reference(x, w, s, z, b, False, out == "bf16"), f"{scales} {out}")
 
 
-@pytest.mark.parametrize("M", [1, 16, 40, 129, 520])
+@pytest.mark.parametrize("M", [1, 16, 40, 129, 200, 520])
 @pytest.mark.parametrize("G,N,K", [(128, 1536, 2048), (64, 258, 320), (32, 2, 96), (32, 130, 128)])
 def test_swiglu(M, G, N, K):
     import block_fp8_routed_amd as moe
@@ -113,7 +117,9 @@ def test_swiglu(M, G, N, K):
 
 
 @pytest.mark.parametrize("M,N,K,G", [(1, 4096, 4096, 128), (16, 512, 8192, 64), (77, 2112, 4096, 32),
-                                     (1000, 640, 1024, 128), (2049, 300, 512, 64)])
+                                     (1000, 640, 1024, 128), (2049, 300, 512, 64),
+                                     (5, 48, 4128, 32), (11, 40, 12288, 128), (200, 4096, 1056, 32),
+                                     (150, 70, 8320, 64), (3000, 2048, 256, 32)])
 def test_long_and_wide_products(M, N, K, G):
     import block_fp8_routed_amd as moe
     w, s, z, _ = weights((), N, K, G, 3, "f32", True)
@@ -132,7 +138,7 @@ def test_every_code_and_zero_point():
     w = torch.from_numpy(np.repeat(codes[:, None], K // 2, axis=1)).cuda()
     zero = torch.from_numpy(np.repeat(z.reshape(-1, 1), 4, axis=1).astype(np.uint8)).cuda()
     s = torch.full((N, 4), 0.5, device="cuda")
-    for M in (1, 128):
+    for M in (1, 128, 256):
         x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
         x[torch.arange(M), torch.arange(M) % K] = 2.0
         want = torch.from_numpy((q - z).reshape(-1).astype(np.float32)).cuda().expand(M, N)
@@ -140,13 +146,13 @@ def test_every_code_and_zero_point():
             assert torch.equal(moe.moe_linear_w4(x, w, s, zero, out_dtype=out), want.to(out))
 
 
-@pytest.mark.parametrize("M", [1, 20, 200])
+@pytest.mark.parametrize("M", [1, 20, 208])
 def test_columns_meet_their_codes(M):
     """x = a unit vector picks one column of W: exact."""
     import block_fp8_routed_amd as moe
     N, K, G = 48, 416, 32
     w, s, z, _ = weights((), N, K, G, 5)
-    v, _ = values(w, s, z)
+    v, _, zero = values(w, s, z)
     for k0 in range(0, K, M):
         x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
         n = min(M, K - k0)
@@ -155,38 +161,65 @@ def test_columns_meet_their_codes(M):
         assert np.array_equal(got.cpu().numpy(), v[:, k0:k0 + n].T.astype(np.float32))
         got = moe.moe_linear_w4(x, w, s, z)[:n].double().cpu().numpy()
         want = v[:, k0:k0 + n].T
-        # two roundings to fp16 (half a step of its 11 bits is 2^-11) and one to bf16
-        # (2^-8): (1 + 2^-11)^2 (1 + 2^-8) - 1 < 2^-8 + 2^-10 + 2^-17
-        assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -10 + 2.0 ** -17) * np.abs(want)).all()
+        # the weight's own error, as above, and its rounding to bf16
+        err = ((1 + 2.0 ** -20) * (2.0 ** -10 * np.abs(want) + 2.0 ** -11 * zero[:, k0:k0 + n].T)
+               + 2.0 ** -14 * s.double().abs().amax(dim=1).cpu().numpy())
+        assert (np.abs(got - want) <= err + 2.0 ** -8 * (np.abs(want) + err)).all()
 
 
-@pytest.mark.parametrize("M", [3, 100])
+@pytest.mark.parametrize("M", [4, 100, 300])
+def test_small_values_beside_a_large_one(M):
+    """A row's small values, down to 2^-24 of its largest, count where the large
+    one's weight is 0."""
+    import block_fp8_routed_amd as moe
+    K, G = 256, 64
+    w, s, _, _ = weights((), 32, K, G, 21, zeros=False)
+    w[:, 50] = 0x88  # columns 100 and 101: 8 - 8
+    s = torch.full_like(s, 0.25)
+    x = activations(M, K, 22)
+    x = (torch.sign(x) * (1 + x.abs() % 1)).to(torch.bfloat16) * 2.0 ** -24
+    x[:, 100] = 1.0
+    for out in TYPES.values():
+        got = moe.moe_linear_w4(x, w, s, out_dtype=out).double().cpu().numpy()
+        small = x.double().cpu().numpy()
+        small[:, 100] = 0
+        want = small @ values(w, s, None)[0].T
+        # Larger batches: 2^-24 is 2^-10 beside 2^14, a normal number of fp16, and 8 - 8 is 0
+        # before it meets x: nothing of the large value is left. Smaller ones sum x q and
+        # 8 x apart: there the large column's two terms of 8 * 0.25 are rounded with the
+        # rest, 2^-24 of 4 each time, which the bound of the whole row counts.
+        seen = torch.from_numpy(small) if M > 192 else x
+        _, err = reference(seen, w, s, None, None, False, out == torch.bfloat16)
+        assert (np.abs(got - want) <= err + HALF[out] * (np.abs(want) + err)).all()
+
+
+@pytest.mark.parametrize("M", [3, 100, 260])
 def test_strided_rows_and_outputs(M):
     import block_fp8_routed_amd as moe
     N, K, G = 70, 256, 64
     w, s, z, _ = weights((), N, K, G, 6)
     x = activations(M, K, 7, pad=24)
     for out in TYPES.values():
-        for pad in (2, 7):
+        for pad in (2, 7, 10):
             whole = torch.full((M, N + pad), 4.0, dtype=out, device="cuda")
             got = moe.moe_linear_w4(x, w, s, z, out=whole[:, 1:N + 1])
             check(got, *reference(x, w, s, z, None, False, out == torch.bfloat16))
             assert bool((whole[:, 0] == 4).all()) and bool((whole[:, N + 1:] == 4).all())
 
 
-@pytest.mark.parametrize("M", [16, 64, 200])
+@pytest.mark.parametrize("M", [16, 64, 200, 2000])
 def test_a_row_of_nan_stays_in_its_row(M):
     import block_fp8_routed_amd as moe
     w, s, z, _ = weights((), 50, 256, 64, 8)
-    x = activations(M, 256, 9)
-    want = moe.moe_linear_w4(x, w, s, z)
-    x[5] = float("nan")
-    x[7, 3] = float("inf")
-    got = moe.moe_linear_w4(x, w, s, z)
-    rest = torch.ones(M, dtype=torch.bool)
-    rest[[5, 7]] = False
-    assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[5]).all())
-    assert not bool(torch.isfinite(got[7]).any())
+    for out in TYPES.values():
+        x = activations(M, 256, 9)
+        want = moe.moe_linear_w4(x, w, s, z, out_dtype=out)
+        x[5] = float("nan")
+        x[7, 3] = float("inf")
+        got = moe.moe_linear_w4(x, w, s, z, out_dtype=out)
+        rest = torch.ones(M, dtype=torch.bool)
+        rest[[5, 7]] = False
+        assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[5]).all())
 
 
 @pytest.mark.parametrize("scale", [2.0 ** 100, 2.0 ** -118])
@@ -194,7 +227,7 @@ def test_ends_of_the_range(scale):
     """Large and small rows, their sums and the scales' products within fp32's range."""
     import block_fp8_routed_amd as moe
     w, s, z, _ = weights((), 40, 256, 128, 10)
-    for M in (2, 90):
+    for M in (2, 90, 250):
         x = (activations(M, 256, 11).float() * scale).to(torch.bfloat16)
         ref, err = reference(x, w, s, z, None, False, False)
         # below 2^-126 fp32 keeps steps of 2^-149, one for each of the roundings
@@ -216,7 +249,7 @@ def grouped_reference(x, offsets, w, s, z, b, swiglu, half=True):
 COUNTS = {
     "one_row": [0, 0, 1, 0], "even": [5, 5, 5, 5], "uneven": [0, 300, 1, 0, 17, 16, 0, 64, 129, 0],
     "single": [140], "none": [0, 0, 0], "last": [0] * 99 + [33], "many": [1, 0, 2] * 230,
-    "tiles": [32, 64, 128, 256, 31, 33, 63, 65],
+    "tiles": [32, 64, 128, 256, 31, 33, 63, 65], "large": [700, 1, 0, 90],
 }
 
 

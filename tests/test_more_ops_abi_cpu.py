@@ -119,7 +119,7 @@ def test_dispatch_workspace():
     (dict(st=2), SHAPE), (dict(out_dtype=-1), SHAPE), (dict(ld_x=255), SHAPE), (dict(ld_out=63), SHAPE),
     (dict(ld_out=31, swiglu=1), SHAPE), (dict(rows=1 << 21), UNSUPPORTED),
     (dict(n=1 << 21, ld_out=1 << 21), UNSUPPORTED), (dict(k=1 << 21, ld_x=1 << 21), UNSUPPORTED),
-    (dict(rows=1 << 20, n=1 << 14, ld_out=1 << 14), UNSUPPORTED),
+    (dict(rows=1 << 20, n=1 << 20, ld_out=1 << 20), UNSUPPORTED),
     (dict(rows=4, x=P + 8), UNSUPPORTED), (dict(rows=4, w=P + 8), UNSUPPORTED),
     (dict(rows=4, ld_x=260), UNSUPPORTED), (dict(rows=4, ws=P + 2), UNSUPPORTED),
     (dict(rows=4, ws=P + 1, st=1), UNSUPPORTED), (dict(rows=4, bias=P + 2), UNSUPPORTED),
@@ -131,11 +131,11 @@ def test_refusals_of_the_products(f, kw, status):
 
 
 def test_product_workspace():
-    assert moe.linear_w4_workspace_bytes(1, 1, 4096, moe.MOE_BF16) == 0
-    n = moe.linear_w4_workspace_bytes(5000, 1, 4000, moe.MOE_BF16)
+    assert moe.linear_w4_workspace_bytes(1, 1, 4096) == 0
+    n = moe.linear_w4_workspace_bytes(5000, 1, 4000)
     assert n >= 5000 * 4000 * 2 and n % 256 == 0
-    for bad in ((-1, 1, 256, 1), (0, 1, 256, 1), (5000, 0, 256, 1), (5000, 1025, 256, 1),
-                (5000, 1, 0, 1), (1 << 21, 1, 256, 1), (5000, 1, 1 << 21, 1)):
+    for bad in ((-1, 1, 256), (0, 1, 256), (5000, 0, 256), (5000, 1025, 256), (5000, 1, 0),
+                (1 << 21, 1, 256), (5000, 1, 1 << 21)):
         assert moe.linear_w4_workspace_bytes(*bad) == 0
 
 
