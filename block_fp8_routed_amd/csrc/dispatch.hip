@@ -54,7 +54,7 @@ __device__ __forceinline__ void st_pack(T* p, const Pack<T, N>& r) {
 }
 
 constexpr int kDispSmall = 4096;   // up to this many slots each workgroup ranks its own token's
-constexpr int kDispChunk = 4096;   // slots a placing workgroup takes, at least
+constexpr int kDispChunk = 1024;   // slots a placing workgroup takes, at least
 constexpr int kDispChunks = 64;    // placing workgroups at most
 
 // -------------------------------------------------------- one launch (small) --
@@ -188,6 +188,7 @@ __global__ __launch_bounds__(1024) void dispatch_place(
   }
   int all[1] = {0}, first[1], total[1], before = 0;
   if (tid < E) {
+#pragma unroll 8
     for (int b = 0; b < (int)gridDim.x; ++b) {
       const int c = counts[(int64_t)b * E + tid];
       if (b < (int)blockIdx.x) before += c;
@@ -410,11 +411,12 @@ static moe_status check_rows(int64_t tokens, int32_t H, int32_t k) {
   return MOE_OK;
 }
 
-// The largest N of 8, 4, 2, 1 elements at which every row of a matrix can be
-// read: N divides the columns and the row distance, the base is aligned.
+// The largest N of 8, 4, 2, 1 elements (4 where all matrices are fp32: 16 bytes) at
+// which every row of a matrix can be read: N divides the columns and the row
+// distance, the base is aligned.
 struct Shape {
-  int n = 8;
-  explicit Shape(int H) { limit(H); }
+  int n;
+  Shape(int H, bool all_f32) : n(all_f32 ? 4 : 8) { limit(H); }
   void limit(int64_t v) {
     while (v % n != 0) n /= 2;
   }
@@ -468,7 +470,7 @@ static moe_status launch_combine_rows(const void* y, int64_t ld_y, int64_t nrows
                                       const float* gates, const int32_t* inv, const void* shared,
                                       int64_t ld_s, int64_t tokens, int H, int k, void* out,
                                       int64_t ld_out, moe_dtype ot, hipStream_t s) {
-  Shape a(H);
+  Shape a(H, yt == MOE_F32 && ot == MOE_F32);
   a.matrix(y, ld_y, yt);
   a.matrix(shared, ld_s, yt);
   a.matrix(out, ld_out, ot);
@@ -523,7 +525,7 @@ moe_status moe_dispatch(const void* x, int64_t ld_x, moe_dtype dtype, const int3
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t TK = tokens * top_k;
   const int H = hidden, k = top_k, E = experts;
-  Shape a(H);
+  Shape a(H, dtype == MOE_F32);
   a.matrix(x, ld_x, dtype);
   a.matrix(rows, ld_rows, dtype);
   if (TK <= kDispSmall) {
@@ -606,7 +608,7 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
     return MOE_ERR_UNSUPPORTED;
   if (tokens == 0) return MOE_OK;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  Shape a(hidden);
+  Shape a(hidden, dtype == MOE_F32 && d_dtype == MOE_F32);
   a.matrix(d_out, ld_d, d_dtype);
   a.matrix(y, ld_y, dtype);
   a.matrix(d_y, ld_dy, dtype);
