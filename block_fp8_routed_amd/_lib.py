@@ -155,7 +155,7 @@ def load() -> ctypes.CDLL:
     lib.moe_combine.argtypes = [P, I64, I64, INT, P, P, P, I64, I64, I32, I32, P, I64, INT, P]
     lib.moe_combine_backward.argtypes = [P, I64, INT, P, I64, I64, INT, P, P, I64, I32, I32, P,
                                          I64, P, P]
-    lib.moe_linear_w4_workspace_bytes.argtypes = [I64, I32, I32]
+    lib.moe_linear_w4_workspace_bytes.argtypes = [I64, I32, I32, I32, INT]
     lib.moe_linear_w4_workspace_bytes.restype = SZ
     lib.moe_linear_w4.argtypes = [P, I64, P, P, INT, P, P, I64, I32, I32, I32, I32, P, I64, INT, P,
                                   SZ, P]
@@ -890,9 +890,11 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, gates: torch.Tens
 
 
 @functools.lru_cache(maxsize=1024)
-def linear_w4_workspace_bytes(rows: int, experts: int, in_features: int) -> int:
-    """moe_linear_w4_workspace_bytes (a function of the sizes alone)."""
-    return int(load().moe_linear_w4_workspace_bytes(rows, experts, in_features))
+def linear_w4_workspace_bytes(rows: int, experts: int, out_features: int, in_features: int,
+                              out_dtype: int) -> int:
+    """moe_linear_w4_workspace_bytes (a function of the sizes and the moe_dtype alone)."""
+    return int(load().moe_linear_w4_workspace_bytes(rows, experts, out_features, in_features,
+                                                    out_dtype))
 
 
 def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, out_dtype, out,
@@ -913,7 +915,7 @@ def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, ou
     _flat(bias, (*lead, N), torch.float32, "bias")
     res, code, ld_out = _result(out, x, M, N // 2 if swiglu else N, out_dtype, stream)
     if workspace is None:
-        need = linear_w4_workspace_bytes(M, lead[0] if lead else 1, K)
+        need = linear_w4_workspace_bytes(M, lead[0] if lead else 1, N, K, code)
         if need:
             workspace = _empty(x, (need,), torch.uint8, stream)
     _enqueue(getattr(_lib or load(), name), name, dev, stream, _addr(x), ld, *head, _addr(w),

@@ -76,8 +76,8 @@ void launch_w4_group32(const W4Args& p, void* workspace, hipStream_t s);
 void launch_w4_group64(const W4Args& p, void* workspace, hipStream_t s);
 void launch_w4_group128(const W4Args& p, void* workspace, hipStream_t s);
 
-static size_t w4_workspace(int64_t M, int E, int K) {
-  if (w4_form(M, E) != kW4Tiles) return 0;
+static size_t w4_workspace(int64_t M, int E, int N, int K, bool bf16) {
+  if (M == 0 || w4_form(M, E, N, K, bf16) != kW4Tiles) return 0;
   return w4_al256((size_t)M * w4_padded(K) * 2) + w4_al256((size_t)M * 4);
 }
 
@@ -99,7 +99,7 @@ static moe_status w4_call(W4Args p, int group, moe_dtype scale_dtype, moe_dtype 
   if (odd(p.x, 16) || odd(p.w, 16) || p.ld_x % 8 != 0 || odd(p.ws, scale_dtype == MOE_BF16 ? 2 : 4) ||
       odd(p.bias, 4) || odd(p.offsets, 4) || odd(p.out, out_dtype == MOE_BF16 ? 2 : 4))
     return MOE_ERR_UNSUPPORTED;
-  const size_t need = w4_workspace(p.M, p.E, p.K);
+  const size_t need = w4_workspace(p.M, p.E, p.N, p.K, out_dtype == MOE_BF16);
   if (need > 0) {
     if (!workspace) return MOE_ERR_NULL;
     if (workspace_bytes < need || odd(workspace, 256)) return MOE_ERR_WORKSPACE;
@@ -119,11 +119,12 @@ using namespace moe;
 
 extern "C" {
 
-size_t moe_linear_w4_workspace_bytes(int64_t rows, int32_t experts, int32_t in_features) {
+size_t moe_linear_w4_workspace_bytes(int64_t rows, int32_t experts, int32_t out_features,
+                                     int32_t in_features, moe_dtype out_dtype) {
   if (rows <= 0 || rows > kW4Limit || experts <= 0 || experts > kMaxExperts || in_features <= 0 ||
-      in_features > kW4Limit)
+      in_features > kW4Limit || out_features <= 0 || out_features > kW4Limit)
     return 0;
-  return w4_workspace(rows, experts, in_features);
+  return w4_workspace(rows, experts, out_features, in_features, out_dtype == MOE_BF16);
 }
 
 moe_status moe_linear_w4(const void* x, int64_t ld_x, const uint8_t* w, const void* w_scales,

@@ -516,156 +516,6 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
   }
 }
 
-// More rows than a stream holds in registers: a workgroup's W wavefronts share 16 FN
-// weight rows and 16 FM rows of x, and split K by units of 128 columns (wavefront w
-// takes every W-th); their sums are joined in LDS in wavefront order. x is read anew
-// for every 16 FN features, from the L2. Operands as above.
-template <int G, bool SB, bool Z, int FM, int FN, int W>
-__global__ __launch_bounds__(64 * W) void w4_rows(W4Args p, int strips) {
-  constexpr int TM = 16 * FM, NG = 128 / G, NB = G / 32, FH = FN / 2;
-  __shared__ float part[W][FM][FN][4][64];
-  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int n_out = p.swiglu ? p.N / 2 : p.N, cols = p.swiglu ? 8 * FN : 16 * FN;
-  const RowTile tile = find_tile<TM>(p, blockIdx.x / strips);
-  if (tile.rows <= 0) return;
-  const int n0 = (int)(blockIdx.x % strips) * cols, groups = p.K / G;
-  const int64_t bank = (int64_t)tile.e * p.N;
-  // this lane's weight row of each tile (rows past the last repeat it)
-  using Scale = std::conditional_t<SB, uint16_t, uint32_t>;
-  const uint8_t* wp[FN];
-  const Scale* sp[FN];
-  const uint8_t* zp[FN];
-#pragma unroll
-  for (int f = 0; f < FN; ++f) {
-    int n = p.swiglu ? n0 + 16 * (f % FH) + l : n0 + 16 * f + l;
-    if (n >= n_out) n = n_out - 1;
-    if (p.swiglu && f >= FH) n += n_out;
-    wp[f] = p.w + (bank + n) * (p.K / 2);
-    sp[f] = static_cast<const Scale*>(p.ws) + (bank + n) * groups;
-    zp[f] = Z ? p.wz + (bank + n) * groups : nullptr;
-  }
-  const uint16_t* xp[FM];
-#pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int r = 16 * f + l < tile.rows ? 16 * f + l : tile.rows - 1;
-    xp[f] = p.x + (tile.r0 + r) * p.ld_x;
-  }
-  bf16x8_t ones;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ones[i] = (__bf16)(1.f / kCodeScale);
-  f32x4 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int f = 0; f < FN; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // the codes and scales of the wavefront's next unit are requested a unit ahead
-  struct Codes {
-    uint4 v[FN];
-    uint32_t s[NG][FN], z[NG][FN];
-  };
-  const auto fetch = [&](int k0, Codes& c) {
-#pragma unroll
-    for (int f = 0; f < FN; ++f) c.v[f] = ld16(wp[f] + (k0 + 32 * q < p.K ? k0 + 32 * q : 0) / 2);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const int at = k0 / G + g < groups ? k0 / G + g : groups - 1;
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        c.s[g][f] = sp[f][at];
-        if (Z) c.z[g][f] = zp[f][at];
-      }
-    }
-  };
-  const auto work = [&](int k0, Codes& c, Codes& next) {
-    const int ahead = k0 + 128 * W < p.K ? k0 + 128 * W : k0;
-    uint4 xv[4][FM];
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-        xv[b][i] = ld16(xp[i] + (k0 + 32 * b < p.K ? k0 + 32 * b : 0) + 8 * q);
-    fetch(ahead, next);
-#pragma unroll
-    for (int f = 0; f < FN; ++f) transpose_quarters(c.v[f]);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      f32x4 d[FM][FN], xs[FM];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        xs[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int f = 0; f < FN; ++f) d[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
-#pragma unroll
-      for (int b = g * NB; b < (g + 1) * NB; ++b) {
-        const bool in = k0 + 32 * b < p.K;  // (what lies behind K counts as zero)
-        bf16x8_t a[FM];
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          a[i] = x_order(in ? xv[b][i] : make_uint4(0, 0, 0, 0));
-          xs[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], ones, xs[i], 0, 0, 0);
-        }
-#pragma unroll
-        for (int f = 0; f < FN; ++f) {
-          const uint32_t cw[4] = {c.v[f].x, c.v[f].y, c.v[f].z, c.v[f].w};
-          const bf16x8_t bw = codes_bf16(cw[b]);
-#pragma unroll
-          for (int i = 0; i < FM; ++i)
-            d[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], bw, d[i][f], 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const float s = __uint_as_float(c.s[g][f] << (SB ? 16 : 0));
-        const float z = Z ? -(float)c.z[g][f] : -8.f;
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            acc[i][f][v] = fmaf(s, fmaf(z, xs[i][v], d[i][f][v]), acc[i][f][v]);
-      }
-    }
-  };
-  int k0 = 128 * w;
-  if (k0 < p.K) {
-    Codes c0, c1;
-    fetch(k0, c0);
-    while (true) {
-      work(k0, c0, c1);
-      if ((k0 += 128 * W) >= p.K) break;
-      work(k0, c1, c0);
-      if ((k0 += 128 * W) >= p.K) break;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int f = 0; f < FN; ++f)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) part[w][i][f][v][lane] = acc[i][f][v];
-  __syncthreads();
-  // value (row 16 i + r, feature 16 f + c) lies at lane 16 (r / 4) + c, v = r % 4
-  const auto total = [&](int i, int f, int r, int c) {
-    float y = 0.f;
-#pragma unroll
-    for (int ww = 0; ww < W; ++ww) y += part[ww][i][f][r & 3][16 * (r >> 2) + c];
-    return y * kCodeScale;
-  };
-  for (int i = threadIdx.x; i < TM * cols; i += 64 * W) {
-    const int r = i / cols, c = i % cols, n = n0 + c;
-    if (r >= tile.rows || n >= n_out) continue;
-    float y = total(r / 16, c / 16, r % 16, c % 16);
-    if (p.bias) y += p.bias[bank + n];
-    if (p.swiglu) {
-      float u = total(r / 16, FH + c / 16, r % 16, c % 16);
-      if (p.bias) u += p.bias[bank + n_out + n];
-      y = w4_silu(y) * u;
-    }
-    w4_store(p, tile.r0 + r, n, y);
-  }
-}
-
 // ------------------------------------------------------------ larger batches --
 // bf16 output of larger batches: both operands become fp16, so that scale and
 // zero point are in the weight itself and the matrix instructions run one chain of
@@ -1122,17 +972,20 @@ inline int64_t row_tiles(const W4Args& p, int TM) {
   return p.offsets ? p.M / TM + (p.M < p.E ? p.M : p.E) : (p.M + TM - 1) / TM;
 }
 
-// Which kernel a product runs on, by its rows and experts (us on one MI355X, weights
-// in no cache, group 128):
-//   up to 16 rows an expert   the stream (128 experts of 1536 x 2048: 16 tokens of 8
-//              experts 31, 256 tokens 66; the rows kernel 49 and 137)
-//   up to 64 rows in all      the rows kernel with 32 rows x 32 features (64 x 4096 x
-//              4096: 15.1; tiles 39)
-//   up to 192                 with 32 x 64 (128 x 4096 x 4096: 22; 32 x 32 27, tiles 39)
-//   above      the tiles (256 x 4096 x 4096: 41; the rows kernel 41)
-enum W4Form { kW4Stream, kW4Rows, kW4Tiles };
-inline W4Form w4_form(int64_t M, int E) {
-  return M <= 16 * (int64_t)E ? kW4Stream : M <= 192 ? kW4Rows : kW4Tiles;
+// Which kernel a product runs on: the one that is reckoned to take less time (us on one
+// MI355X, weights in no cache). The weights of the experts that can have a row, read
+// once, take W = E N K / 10^7.
+//   stream  8 + 5.4e-9 M N K + 0.75 W   (4096 x 4096, 128 / 512 / 1024 rows: 21 / 54 / 99; 128
+//           experts of 2048 x 2048, 32 / 64 / 96 rows each: 143 / 233 / 331)
+//   tiles   10 + 2.5e-9 (M + 32 E) N K + W, at least 6 + 1.45 a stage + W; fp32 output 2.9e-9
+//           (M + 48 E): E short tiles (54 / 57 / 63, fp32 52 / 56 / 68; 146 / 190 / 241, fp32 169 / 238 / 284)
+enum W4Form { kW4Stream, kW4Tiles };
+inline W4Form w4_form(int64_t M, int E, int N, int K, bool bf16) {
+  const double experts = (double)(M < E ? M : E), NK = (double)N * K, W = experts * NK * 1e-7;
+  const double stream = 8.0 + 5.4e-9 * M * NK + 0.75 * W;
+  const double busy = 10.0 + (bf16 ? 2.5e-9 * (M + 32 * experts) : 2.9e-9 * (M + 48 * experts)) * NK;
+  const double stages = 6.0 + 1.45 * ((K + kW4Stage - 1) / kW4Stage);
+  return stream <= W + (busy > stages ? busy : stages) ? kW4Stream : kW4Tiles;
 }
 
 inline int w4_padded(int K) { return (K + kW4Stage - 1) / kW4Stage * kW4Stage; }
@@ -1148,21 +1001,16 @@ void launch_stream(const W4Args& p, hipStream_t s) {
       <<<(unsigned)(most < kGrid ? most : kGrid), 64 * W, 0, s>>>(p);
 }
 
-template <int G, bool SB, bool Z, int FM, int FN, int W>
-void launch_rows(const W4Args& p, hipStream_t s) {
-  const int cols = p.swiglu ? 8 * FN : 16 * FN, strips = ((p.swiglu ? p.N / 2 : p.N) + cols - 1) / cols;
-  w4_rows<G, SB, Z, FM, FN, W><<<(unsigned)(row_tiles(p, 16 * FM) * strips), 64 * W, 0, s>>>(p, strips);
-}
-
 // Tiles of 32 FM rows whose rounds of workgroups cost least. A stage of a round takes,
 // with two workgroups on every compute unit, 1.55 us at FM = 1, 2.3 at 2, 4.0 at 4; 1.1,
-// 1.25 and 1.95 with one at most (bf16 output; fp32 output EXACTCOST).
+// 1.25 and 1.95 with one at most (fp32 output: 1.6 and 2.35, 1.2 and 1.3).
 // By expert, half a tile for each is reckoned as its short one.
 template <bool EXACT>
 int best_tile(const W4Args& p) {
   const int cols = p.swiglu ? 128 : 256;
   const double strips = ((p.swiglu ? p.N / 2 : p.N) + cols - 1) / cols;
-  const double full[2][3] = {{1.55, 2.3, 4.0}, {1.9, 3.2, 0}}, alone[2][3] = {{1.1, 1.25, 1.95}, {1.2, 1.6, 0}};
+  const double full[2][3] = {{1.55, 2.3, 4.0}, {1.6, 2.35, 0}},
+               alone[2][3] = {{1.1, 1.25, 1.95}, {1.2, 1.3, 0}};
   int best = 1;
   double least = 0;
   for (int i = 0; i < (EXACT ? 2 : 3); ++i) {
@@ -1193,7 +1041,7 @@ void launch_tile(const W4Args& p, const uint16_t* xh, const int32_t* xe, hipStre
 
 template <int G, bool SB, bool Z>
 void launch_w4(const W4Args& p, void* workspace, hipStream_t s) {
-  const W4Form form = w4_form(p.M, p.E);
+  const W4Form form = w4_form(p.M, p.E, p.N, p.K, p.out_bf16);
   if (form == kW4Stream) {
     // wavefronts and units that cover K with the fewest idle ones (1024 columns: 2 x 4 37
     // us, 4 x 2 41, 8 x 1 50; 2048: 4 x 4 30, 8 x 2 36; 4096: 8 x 4 64, 16 x 2 72)
@@ -1202,11 +1050,6 @@ void launch_w4(const W4Args& p, void* workspace, hipStream_t s) {
     if (p.K <= 2048) return launch_stream<G, SB, Z, 4, 4, false>(p, s);
     if (p.K <= 4096) return launch_stream<G, SB, Z, 8, 4, false>(p, s);
     return launch_stream<G, SB, Z, 8, 4, true>(p, s);
-  }
-  if (form == kW4Rows) {
-    // (groups of 32 columns: 32 x 64 would spill registers)
-    if (G == 32 || p.M <= 64) return launch_rows<G, SB, Z, 2, 2, 8>(p, s);
-    return launch_rows<G, SB, Z, 2, G == 32 ? 2 : 4, 8>(p, s);
   }
   const int Kp = w4_padded(p.K);
   uint4* xh = static_cast<uint4*>(workspace);

@@ -500,8 +500,7 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  * expert e (offsets[e] <= t < offsets[e+1]) is multiplied with that expert's
  * matrix. With swiglu = 1 the first half of the features are gates g and the
  * second half u, and out[t][i] = silu(g_i) * u_i of out_features / 2 columns.
- * x is multiplied as it is; sums, scales and zero points are fp32, rounded once
- * to the output type. (zilda page, "Roadmap", and colizig page, "Status", name
+ * x is multiplied as it is, in fp32 sums that are rounded once to the output type. (zilda page, "Roadmap", and colizig page, "Status", name
  * 4-bit weights as a coming step; the format is a reading of this project.)
  *   x        [rows] rows of in_features bf16 values, finite, ld_x elements apart
  *            (a multiple of 8, at least in_features), 16-byte aligned
@@ -519,10 +518,17 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  *            overlaps no input
  * (experts: without it for moe_linear_w4.) group is 32, 64 or 128 and divides
  * in_features; out_features is free, but even with swiglu. A row's result does not
- * depend on the other rows' values. in_features, out_features, rows <= 2^20 and
- * ceil(rows/16) * ceil(out_features/16) < 2^23, by expert with experts more tiles of
- * rows (else MOE_ERR_UNSUPPORTED). rows == 0 enqueues nothing. */
-size_t moe_linear_w4_workspace_bytes(int64_t rows, int32_t experts, int32_t in_features);
+ * depend on the other rows' values; which kernel a call takes goes by its sizes
+ * and output type. Larger batches with bf16 output multiply with weights rounded to
+ * fp16, an error of at most (2^-10 |q - z| + 2^-11 z) s and 2^-14 of the row's largest
+ * scale in each weight, 3e-4 of the result in norm beside the 1.7e-3 of its rounding
+ * to bf16; all else is exact up to fp32's own rounding. experts <= 1024;
+ * in_features, out_features, rows <= 2^20; (rows/32 + experts) * ceil(out_features/128)
+ * < 2^24 (else MOE_ERR_UNSUPPORTED). rows == 0 enqueues nothing. The workspace is
+ * moe_linear_w4_workspace_bytes() of the same sizes, experts = 1 for moe_linear_w4 (0
+ * bytes: NULL is allowed), 256-byte aligned; calls that overlap need one each. */
+size_t moe_linear_w4_workspace_bytes(int64_t rows, int32_t experts, int32_t out_features,
+                                     int32_t in_features, moe_dtype out_dtype);
 moe_status moe_linear_w4(const void* x, int64_t ld_x, const uint8_t* w, const void* w_scales,
                          moe_dtype scale_dtype, const uint8_t* w_zeros, const float* bias,
                          int64_t rows, int32_t out_features, int32_t in_features, int32_t group,

@@ -88,6 +88,13 @@ def check(got, ref, err, what=""):
     assert (off <= lim).all(), f"{what}: {np.max(off / lim):.2f} of the bound"
 
 
+def takes_tiles(M, N, K, out, E=1):
+    """Whether a product runs on the tiles of larger batches (they alone have a workspace)."""
+    import block_fp8_routed_amd as moe
+    code = moe.MOE_BF16 if out == torch.bfloat16 else moe.MOE_F32
+    return moe.linear_w4_workspace_bytes(M, E, N, K, code) > 0
+
+
 ROWS = [1, 2, 15, 16, 17, 33, 64, 65, 130, 193, 300]
 
 
@@ -102,6 +109,22 @@ def test_product(M, G, N, K):
         x = activations(M, K, M)
         got = moe.moe_linear_w4(x, w, s, z, bias=b, out_dtype=TYPES[out])
         check(got, *reference(x, w, s, z, b, False, out == "bf16"), f"{scales} {out}")
+
+
+@pytest.mark.parametrize("M,N,K,G", [(4100, 420, 512, 128), (4133, 702, 352, 32), (3000, 1026, 320, 64),
+                                     (2049, 1030, 1056, 32), (1500, 4096, 256, 128), (700, 4096, 1024, 64),
+                                     (20000, 130, 512, 128), (30001, 66, 1088, 64), (20000, 2048, 32, 32)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_products_of_larger_batches(M, N, K, G, swiglu):
+    import block_fp8_routed_amd as moe
+    N += swiglu and N % 2
+    for i, out in enumerate(TYPES.values()):
+        assert takes_tiles(M, N, K, out)
+        w, s, z, b = weights((), N, K, G, M + i, "bf16" if i else "f32", i == M % 2, M % 3 > 0)
+        x = activations(M, K, M)
+        s = s * 0.1 if swiglu else s
+        got = moe.moe_linear_w4(x, w, s, z, bias=b, swiglu=swiglu, out_dtype=out)
+        check(got, *reference(x, w, s, z, b, swiglu, out == torch.bfloat16), str(out))
 
 
 @pytest.mark.parametrize("M", [1, 16, 40, 129, 200, 520])
@@ -138,7 +161,7 @@ def test_every_code_and_zero_point():
     w = torch.from_numpy(np.repeat(codes[:, None], K // 2, axis=1)).cuda()
     zero = torch.from_numpy(np.repeat(z.reshape(-1, 1), 4, axis=1).astype(np.uint8)).cuda()
     s = torch.full((N, 4), 0.5, device="cuda")
-    for M in (1, 128, 256):
+    for M in (1, 128, 1700):
         x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
         x[torch.arange(M), torch.arange(M) % K] = 2.0
         want = torch.from_numpy((q - z).reshape(-1).astype(np.float32)).cuda().expand(M, N)
@@ -146,11 +169,11 @@ def test_every_code_and_zero_point():
             assert torch.equal(moe.moe_linear_w4(x, w, s, zero, out_dtype=out), want.to(out))
 
 
-@pytest.mark.parametrize("M", [1, 20, 208])
+@pytest.mark.parametrize("M", [1, 20, 208, 1100])
 def test_columns_meet_their_codes(M):
     """x = a unit vector picks one column of W: exact."""
     import block_fp8_routed_amd as moe
-    N, K, G = 48, 416, 32
+    N, K, G = 48 if M < 1000 else 2100, 416, 32
     w, s, z, _ = weights((), N, K, G, 5)
     v, _, zero = values(w, s, z)
     for k0 in range(0, K, M):
@@ -167,13 +190,13 @@ def test_columns_meet_their_codes(M):
         assert (np.abs(got - want) <= err + 2.0 ** -8 * (np.abs(want) + err)).all()
 
 
-@pytest.mark.parametrize("M", [4, 100, 300])
+@pytest.mark.parametrize("M", [4, 100, 4100])
 def test_small_values_beside_a_large_one(M):
     """A row's small values, down to 2^-24 of its largest, count where the large
     one's weight is 0."""
     import block_fp8_routed_amd as moe
-    K, G = 256, 64
-    w, s, _, _ = weights((), 32, K, G, 21, zeros=False)
+    N, K, G = 32 if M < 4000 else 900, 256, 64
+    w, s, _, _ = weights((), N, K, G, 21, zeros=False)
     w[:, 50] = 0x88  # columns 100 and 101: 8 - 8
     s = torch.full_like(s, 0.25)
     x = activations(M, K, 22)
@@ -188,15 +211,15 @@ def test_small_values_beside_a_large_one(M):
         # before it meets x: nothing of the large value is left. Smaller ones sum x q and
         # 8 x apart: there the large column's two terms of 8 * 0.25 are rounded with the
         # rest, 2^-24 of 4 each time, which the bound of the whole row counts.
-        seen = torch.from_numpy(small) if M > 192 else x
+        seen = torch.from_numpy(small) if takes_tiles(M, N, K, out) else x
         _, err = reference(seen, w, s, None, None, False, out == torch.bfloat16)
         assert (np.abs(got - want) <= err + HALF[out] * (np.abs(want) + err)).all()
 
 
-@pytest.mark.parametrize("M", [3, 100, 260])
+@pytest.mark.parametrize("M", [3, 100, 4100])
 def test_strided_rows_and_outputs(M):
     import block_fp8_routed_amd as moe
-    N, K, G = 70, 256, 64
+    N, K, G = 70 if M < 4000 else 910, 256, 64
     w, s, z, _ = weights((), N, K, G, 6)
     x = activations(M, K, 7, pad=24)
     for out in TYPES.values():
@@ -207,10 +230,10 @@ def test_strided_rows_and_outputs(M):
             assert bool((whole[:, 0] == 4).all()) and bool((whole[:, N + 1:] == 4).all())
 
 
-@pytest.mark.parametrize("M", [16, 64, 200, 2000])
+@pytest.mark.parametrize("M", [16, 64, 200, 4100])
 def test_a_row_of_nan_stays_in_its_row(M):
     import block_fp8_routed_amd as moe
-    w, s, z, _ = weights((), 50, 256, 64, 8)
+    w, s, z, _ = weights((), 50 if M < 4000 else 900, 256, 64, 8)
     for out in TYPES.values():
         x = activations(M, 256, 9)
         want = moe.moe_linear_w4(x, w, s, z, out_dtype=out)
@@ -226,8 +249,8 @@ def test_a_row_of_nan_stays_in_its_row(M):
 def test_ends_of_the_range(scale):
     """Large and small rows, their sums and the scales' products within fp32's range."""
     import block_fp8_routed_amd as moe
-    w, s, z, _ = weights((), 40, 256, 128, 10)
-    for M in (2, 90, 250):
+    for M, N in ((2, 40), (90, 40), (4100, 900)):
+        w, s, z, _ = weights((), N, 256, 128, 10)
         x = (activations(M, 256, 11).float() * scale).to(torch.bfloat16)
         ref, err = reference(x, w, s, z, None, False, False)
         # below 2^-126 fp32 keeps steps of 2^-149, one for each of the roundings
@@ -249,7 +272,8 @@ def grouped_reference(x, offsets, w, s, z, b, swiglu, half=True):
 COUNTS = {
     "one_row": [0, 0, 1, 0], "even": [5, 5, 5, 5], "uneven": [0, 300, 1, 0, 17, 16, 0, 64, 129, 0],
     "single": [140], "none": [0, 0, 0], "last": [0] * 99 + [33], "many": [1, 0, 2] * 230,
-    "tiles": [32, 64, 128, 256, 31, 33, 63, 65], "large": [700, 1, 0, 90],
+    "tiles": [32, 64, 128, 256, 31, 33, 63, 65],
+    "large": [700, 1, 0, 90, 1300, 31, 33, 64, 65, 2200, 0, 0],
 }
 
 
@@ -259,7 +283,7 @@ COUNTS = {
 def test_grouped(name, swiglu, G):
     import block_fp8_routed_amd as moe
     counts = COUNTS[name]
-    E, N, K = len(counts), 72, 256
+    E, N, K = len(counts), 72 if name != "large" else 1030, 256
     offsets = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
     behind = 7  # rows of no expert
     M = int(offsets[-1]) + behind
@@ -267,7 +291,9 @@ def test_grouped(name, swiglu, G):
     s = s * 0.1
     x = activations(M, K, 13)
     n = N // 2 if swiglu else N
-    out = torch.full((M, n), 6.0, dtype=torch.bfloat16 if swiglu else torch.float32, device="cuda")
+    kind = torch.bfloat16 if swiglu else torch.float32
+    assert takes_tiles(M, N, K, kind, E) == (name == "large")
+    out = torch.full((M, n), 6.0, dtype=kind, device="cuda")
     got = moe.moe_grouped_linear_w4(x, torch.from_numpy(offsets).cuda(), w, s, z, bias=b,
                                     swiglu=swiglu, out=out)
     ref, err = grouped_reference(x, offsets, w, s, z, b, swiglu, swiglu)
@@ -275,10 +301,10 @@ def test_grouped(name, swiglu, G):
     assert bool((out[M - behind:] == 6).all())
 
 
-def test_offsets_are_cut_to_the_rows():
+@pytest.mark.parametrize("M,N,K", [(40, 32, 128), (4100, 1030, 256)])
+def test_offsets_are_cut_to_the_rows(M, N, K):
     """Offsets beyond the rows, negative or falling name no row outside x and out."""
     import block_fp8_routed_amd as moe
-    M, N, K = 40, 32, 128
     w, s, z, _ = weights((4,), N, K, 128, 14)
     x = activations(M, K, 15)
     out = torch.full((M, N), 6.0, dtype=torch.float32, device="cuda")
@@ -294,8 +320,8 @@ def test_offsets_are_cut_to_the_rows():
 def test_a_row_does_not_depend_on_the_batch_of_one_kernel():
     """Rows of a batch of one size keep their bits whatever the other rows hold."""
     import block_fp8_routed_amd as moe
-    w, s, z, _ = weights((), 100, 512, 64, 16)
-    for M in (16, 100, 600):
+    for M, N in ((16, 100), (100, 100), (4100, 700)):
+        w, s, z, _ = weights((), N, 512, 64, 16)
         x = activations(M, 512, 17)
         y = x.clone()
         y[M // 2:] = activations(M - M // 2, 512, 18) * 100
@@ -306,7 +332,8 @@ def test_a_row_does_not_depend_on_the_batch_of_one_kernel():
             assert torch.equal(b, moe.moe_linear_w4(y, w, s, z, out_dtype=out))
 
 
-@pytest.mark.parametrize("T,E,k,H,I", [(1, 512, 10, 256, 128), (16, 128, 8, 512, 192), (300, 8, 2, 256, 160)])
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 512, 10, 256, 128), (16, 128, 8, 512, 192), (300, 8, 2, 256, 160),
+                                        (2500, 8, 2, 512, 512)])
 @pytest.mark.parametrize("share", [False, True])
 def test_layer_of_4_bit_experts(T, E, k, H, I, share):
     """dispatch, gate/up with SwiGLU, down, combine, as they are used together; and

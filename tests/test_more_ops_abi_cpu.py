@@ -124,18 +124,20 @@ def test_dispatch_workspace():
     (dict(rows=4, ld_x=260), UNSUPPORTED), (dict(rows=4, ws=P + 2), UNSUPPORTED),
     (dict(rows=4, ws=P + 1, st=1), UNSUPPORTED), (dict(rows=4, bias=P + 2), UNSUPPORTED),
     (dict(rows=4, out=P + 1), UNSUPPORTED), (dict(rows=4, out=P + 2, out_dtype=0), UNSUPPORTED),
-    (dict(rows=5000), NULL), (dict(rows=5000, work=P, work_bytes=1000), WORKSPACE),
-    (dict(rows=5000, work=P + 16, work_bytes=1 << 30), WORKSPACE)])
+    (dict(rows=50000, n=1024, ld_out=1024), NULL),
+    (dict(rows=50000, n=1024, ld_out=1024, work=P, work_bytes=1000), WORKSPACE),
+    (dict(rows=50000, n=1024, ld_out=1024, work=P + 16, work_bytes=1 << 30), WORKSPACE)])
 def test_refusals_of_the_products(f, kw, status):
     assert f(**kw) == status
 
 
 def test_product_workspace():
-    assert moe.linear_w4_workspace_bytes(1, 1, 4096) == 0
-    n = moe.linear_w4_workspace_bytes(5000, 1, 4000)
+    assert moe.linear_w4_workspace_bytes(1, 1, 4096, 4096, moe.MOE_BF16) == 0
+    n = moe.linear_w4_workspace_bytes(5000, 1, 4096, 4000, moe.MOE_BF16)
     assert n >= 5000 * 4000 * 2 and n % 256 == 0
-    for bad in ((-1, 1, 256), (0, 1, 256), (5000, 0, 256), (5000, 1025, 256), (5000, 1, 0),
-                (1 << 21, 1, 256), (5000, 1, 1 << 21)):
+    for bad in ((-1, 1, 4096, 256, 1), (0, 1, 4096, 256, 1), (5000, 0, 4096, 256, 1),
+                (5000, 1025, 4096, 256, 1), (5000, 1, 4096, 0, 1), (1 << 21, 1, 4096, 256, 1),
+                (5000, 1, 4096, 1 << 21, 1), (5000, 1, 0, 256, 1), (5000, 1, 1 << 21, 256, 1)):
         assert moe.linear_w4_workspace_bytes(*bad) == 0
 
 
