@@ -223,7 +223,7 @@ __device__ __forceinline__ uint32_t lds_offset(T* p) {
 }
 
 // Few rows: a stream of the weights. All strips of 16 weight rows of all tiles of
-// 16 FM rows are shared out evenly among the workgroups, so that each takes runs of
+// 16 rows are shared out evenly among the workgroups, so that each takes runs of
 // strips of one tile, or two. A workgroup's W wavefronts share K, UW units of 128
 // columns each, whose x they hold in registers for a run (if K is longer than W UW
 // units, in several passes a strip, x read again). A strip's codes, scales and zero
@@ -256,12 +256,11 @@ struct StreamRing {
 };
 template <int G, bool SB, bool Z, int W, int UW, int KB, bool LONG>
 __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
-  constexpr int FM = 1;  // tiles of rows
   using R = StreamRing<G, Z, W, UW, KB>;
   constexpr int D = R::D;
-  constexpr int TM = 16 * FM, NG = 128 / G, NB = G / 32, kOut = (TM * 16 + 64 * W - 1) / (64 * W);
+  constexpr int TM = 16, NG = 128 / G, NB = G / 32, kOut = (TM * 16 + 64 * W - 1) / (64 * W);
   __shared__ __attribute__((aligned(16))) uint8_t ring[R::kBytes];
-  __shared__ float part[2][W][FM][4][64];
+  __shared__ float part[2][W][4][64];
   __shared__ __attribute__((aligned(16))) int32_t plan[4];  // tiles; the tile in hand
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -361,47 +360,41 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
       const float* bp = p.bias ? p.bias : reinterpret_cast<const float*>(p.w);
       lds4<4>(to + R::kBias, bp + n, 4u * (uint32_t)row(l));
     };
-    const uint16_t* xp[FM];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int r = 16 * i + l < tile.rows ? 16 * i + l : tile.rows - 1;
-      xp[i] = p.x + (tile.r0 + r) * p.ld_x;
-    }
+    const uint16_t* xp = p.x + (tile.r0 + (l < tile.rows ? l : tile.rows - 1)) * p.ld_x;
     // x in the codes' order, and the groups' sums (without zero points: times -8, what
     // a group's product starts from)
     // (groups of 32 columns: 64 registers; there the instruction is repeated instead)
     constexpr bool kHeld = G > 32;
-    bf16x8_t a[UW][4][FM];
-    f32x4 xs[kHeld ? UW : 1][NG][FM];
+    bf16x8_t a[UW][4];
+    f32x4 xs[kHeld ? UW : 1][NG];
     const auto load_x = [&](int pass) {
-      uint4 v[UW][4][FM];
 #pragma unroll
-      for (int u = 0; u < UW; ++u)
+      for (int u0 = 0; u0 < UW; u0 += 2) {  // (two units under way: registers)
+        uint4 v[2][4];
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int u = u0; u < u0 + 2 && u < UW; ++u)
 #pragma unroll
-          for (int i = 0; i < FM; ++i) {
+          for (int b = 0; b < 4; ++b) {
             const int k = unit(pass, u) + 32 * b;
-            v[u][b][i] = make_uint4(0, 0, 0, 0);
-            if (k < p.K) v[u][b][i] = ld16(xp[i] + k + 8 * q);
+            v[u - u0][b] = make_uint4(0, 0, 0, 0);
+            if (k < p.K) v[u - u0][b] = ld16(xp + k + 8 * q);
           }
 #pragma unroll
-      for (int u = 0; u < UW; ++u)
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
+        for (int u = u0; u < u0 + 2 && u < UW; ++u)
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int b = g * NB; b < (g + 1) * NB; ++b) {
-              a[u][b][i] = x_order(v[u][b][i]);
-              if (kHeld) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][b][i], ones, sum, 0, 0, 0);
+              a[u][b] = x_order(v[u - u0][b]);
+              if (kHeld) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][b], ones, sum, 0, 0, 0);
             }
             if (kHeld) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) xs[u][g][i][j] = Z ? sum[j] : -8.f * sum[j];
+              for (int j = 0; j < 4; ++j) xs[u][g][j] = Z ? sum[j] : -8.f * sum[j];
             }
           }
+      }
     };
     At at{s0, 0, 0}, ahead = at;
     int issued = 0, done = 0;
@@ -412,9 +405,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
       step(ahead);
     }
     load_x(0);
-    f32x4 acc[FM];
-#pragma unroll
-    for (int i = 0; i < FM; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     float gate[kOut];
 #pragma unroll 1
     for (; done < items; ++done) {
@@ -425,22 +416,8 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
         w4_wait<0>();
       const uint8_t* from = mine + buffer * R::kSlot;
       uint4 code[UW];
-      float s[R::kScaleLoads * 4], z[R::kScaleLoads * 4];
 #pragma unroll
       for (int u = 0; u < UW; ++u) code[u] = *reinterpret_cast<const uint4*>(from + 1024 * u + 16 * lane);
-#pragma unroll
-      for (int i = 0; i < R::kScaleLoads; ++i) {
-        const uint4 sv = *reinterpret_cast<const uint4*>(from + R::kScales + 256 * i + 16 * l);
-        const uint32_t raw[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[4 * i + j] = __uint_as_float(raw[j] << (SB ? 16 : 0));
-        if (Z) {
-          const uint4 zv = *reinterpret_cast<const uint4*>(from + R::kZeros + 256 * i + 16 * l);
-          const uint32_t raz[4] = {zv.x, zv.y, zv.z, zv.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) z[4 * i + j] = -(float)raz[j];
-        }
-      }
       const float bias = *reinterpret_cast<const float*>(from + R::kBias + 4 * l);
       // (the buffer before this one has been read: w4_wait)
       if (issued < items) {
@@ -449,55 +426,55 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
         ++issued;
       }
       buffer = buffer + 1 == D ? 0 : buffer + 1;
+      uint32_t s4[4], z4[4];  // raw scales and zero points of four groups
 #pragma unroll
       for (int u = 0; u < UW; ++u) {
         transpose_quarters(code[u]);
         const uint32_t cw[4] = {code[u].x, code[u].y, code[u].z, code[u].w};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          f32x4 d[FM];
-#pragma unroll
-          for (int i = 0; i < FM; ++i) {
-            if (!kHeld) asm volatile("" : "+v"(ones));  // (or it is done ahead, and held)
-            if (!kHeld)
-              xs[0][g][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  a[u][g][i], ones, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-            d[i] = Z ? f32x4{0.f, 0.f, 0.f, 0.f} : xs[kHeld ? u : 0][g][i];
+          const int at4 = u * NG + g;
+          if (at4 % 4 == 0) {
+            const uint4 sv = *reinterpret_cast<const uint4*>(from + R::kScales + 64 * at4 + 16 * l);
+            s4[0] = sv.x, s4[1] = sv.y, s4[2] = sv.z, s4[3] = sv.w;
+            if (Z) {
+              const uint4 zv = *reinterpret_cast<const uint4*>(from + R::kZeros + 64 * at4 + 16 * l);
+              z4[0] = zv.x, z4[1] = zv.y, z4[2] = zv.z, z4[3] = zv.w;
+            }
           }
-#pragma unroll
-          for (int b = g * NB; b < (g + 1) * NB; ++b) {
-            const bf16x8_t bw = codes_bf16(cw[b]);
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-              d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][b][i], bw, d[i], 0, 0, 0);
+          f32x4 xg;
+          if (kHeld) {
+            xg = xs[kHeld ? u : 0][g];
+          } else {
+            asm volatile("" : "+v"(ones));  // (or it is done ahead, and held)
+            xg = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][g], ones, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
           }
-          const float sv = s[u * NG + g];
+          f32x4 d = Z ? f32x4{0.f, 0.f, 0.f, 0.f} : xg;
 #pragma unroll
-          for (int i = 0; i < FM; ++i)
+          for (int b = g * NB; b < (g + 1) * NB; ++b)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[u][b], codes_bf16(cw[b]), d, 0, 0, 0);
+          const float sv = __uint_as_float(s4[at4 % 4] << (SB ? 16 : 0));
+          const float zv = Z ? -(float)z4[at4 % 4] : 0.f;
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
-              acc[i][v] = fmaf(sv, Z ? fmaf(z[u * NG + g], xs[kHeld ? u : 0][g][i][v], d[i][v]) : d[i][v],
-                               acc[i][v]);
+          for (int v = 0; v < 4; ++v) acc[v] = fmaf(sv, Z ? fmaf(zv, xg[v], d[v]) : d[v], acc[v]);
         }
       }
       if (at.pass + 1 == passes) {
-        float (*buf)[FM][4][64] = part[(at.strip * per + at.half) & 1];
+        float (*buf)[4][64] = part[(at.strip * per + at.half) & 1];
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            buf[w][i][v][lane] = acc[i][v];
-            acc[i][v] = 0.f;
-          }
+        for (int v = 0; v < 4; ++v) {
+          buf[w][v][lane] = acc[v];
+          acc[v] = 0.f;
+        }
         lds_barrier();  // (a buffer is written again only behind the next strip's barrier)
-        // value (row 16 i + r, feature c) lies at lane 16 (r / 4) + c, v = r % 4
+        // value (row r, feature c) lies at lane 16 (r / 4) + c, v = r % 4
 #pragma unroll
         for (int o = 0; o < kOut; ++o) {
           const int i = tid + 64 * W * o, r = i / 16, n = 16 * at.strip + l;
           if (r >= tile.rows || n >= n_out) continue;
           float y = 0.f;
 #pragma unroll
-          for (int ww = 0; ww < W; ++ww) y += buf[ww][r / 16][r & 3][16 * ((r & 15) >> 2) + l];
+          for (int ww = 0; ww < W; ++ww) y += buf[ww][r & 3][16 * (r >> 2) + l];
           y *= kCodeScale;
           if (p.bias) y += bias;
           if (per == 2) {
