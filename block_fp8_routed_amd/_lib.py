@@ -757,29 +757,36 @@ def moe_swiglu_quantize_e4m3(gate_up: torch.Tensor, stream=None):
 
 
 # ---- rows to their experts and back, and products with 4-bit weights ----
-def _matrix(t: torch.Tensor, cols: int, what: str):
-    """(moe_dtype, distance of rows) of a 2-D fp32 or bf16 tensor of `cols` columns."""
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None:
+# (At decode sizes a call's checks take longer than its kernel: tensors are asked
+# for each property once.)
+def _matrix(t: torch.Tensor, what: str):
+    """(rows, columns, distance of rows, moe_dtype) of a 2-D fp32 or bf16 tensor with
+    contiguous rows."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what} must be float32 or bfloat16")
-    ld = _rows(t, what)
-    if t.shape[1] != cols:
-        raise ValueError(f"{what} must have {cols} columns")
-    return dtype, ld
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D with contiguous rows")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{what} must be 2-D with contiguous rows")
+    return rows, cols, ld if rows > 1 else cols, code
 
 
-def _result(out: Optional[torch.Tensor], like: torch.Tensor, rows: int, cols: int, dtype, stream,
-            what: str = "out"):
-    """(tensor, moe_dtype, distance of rows): `out`, or a new tensor of `dtype`."""
+def _result(out: Optional[torch.Tensor], like: torch.Tensor, rows: int, cols: int, dtype, stream):
+    """(tensor, distance of rows, moe_dtype): `out`, or a new tensor of `dtype`."""
     if out is None:
         code = _DTYPES.get(dtype)
         if code is None:
             raise ValueError(f"unsupported dtype {dtype}")
-        return _empty(like, (rows, cols), dtype, stream), code, cols
-    code, ld = _matrix(out, cols, what)
-    if out.shape[0] != rows:
-        raise ValueError(f"{what} must have {rows} rows")
-    return out, code, ld
+        if stream is None:
+            return like.new_empty((rows, cols), dtype=dtype), cols, code
+        return _empty(like, (rows, cols), dtype, stream), cols, code
+    r, c, ld, code = _matrix(out, "out")
+    if r != rows or c != cols:
+        raise ValueError(f"out must have the shape {(rows, cols)}")
+    return out, ld, code
 
 
 def _slots(inv: torch.Tensor):
@@ -802,26 +809,29 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, experts: int,
     inv [T][k], all int32). Choices outside [0, experts) get no row (inv -1); rows
     behind offsets[experts] are left as they were (pair -1)."""
     dev = _place(x, topk_idx, out, workspace)
-    if x.dim() != 2 or topk_idx.dim() != 2:
-        raise ValueError("x and topk_idx must be 2-D")
-    T, H = x.shape
-    dtype, ld = _matrix(x, H, "x")
+    T, H, ld, dtype = _matrix(x, "x")
+    if topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be 2-D")
     k = topk_idx.shape[1]
     _flat(topk_idx, (T, k), torch.int32, "topk_idx")
-    rows, code, ld_rows = _result(out, x, T * k, H, x.dtype, stream)
+    rows, ld_rows, code = _result(out, x, T * k, H, x.dtype, stream)
     if code != dtype:
         raise ValueError("out must have x's type")
-    offsets = _empty(topk_idx, (max(experts, 0) + 1,), torch.int32, stream)
-    pair = _empty(topk_idx, (T * k,), torch.int32, stream)
-    inv = _empty(topk_idx, (T, k), torch.int32, stream)
+    # offsets, pair and inv in one allocation
+    first, slots = max(experts, 0) + 1, T * k
+    at_pair, at_inv = (first + 63) // 64 * 64, (first + 63) // 64 * 64 + (slots + 63) // 64 * 64
+    index = _empty(topk_idx, (at_inv + slots,), torch.int32, stream)
+    base = index.data_ptr()
     if workspace is None:
         need = dispatch_workspace_bytes(T, k, experts)
         if need:
             workspace = _empty(x, (need,), torch.uint8, stream)
-    _enqueue((_lib or load()).moe_dispatch, "moe_dispatch", dev, stream, _addr(x), ld, dtype,
-             _addr(topk_idx), T, H, k, experts, _addr(rows), ld_rows, _addr(offsets), _addr(pair),
-             _addr(inv), _addr(workspace), _bytes(workspace))
-    return rows, offsets, pair, inv
+    _enqueue((_lib or load()).moe_dispatch, "moe_dispatch", dev, stream, x.data_ptr() or _UNREAD,
+             ld, dtype, topk_idx.data_ptr() or _UNREAD, T, H, k, experts,
+             rows.data_ptr() or _UNREAD, ld_rows, base, base + 4 * at_pair, base + 4 * at_inv,
+             _addr(workspace), _bytes(workspace))
+    return (rows, index.as_strided((first,), (1,)), index.as_strided((slots,), (1,), at_pair),
+            index.as_strided((T, k), (k, 1), at_inv))
 
 
 def moe_dispatch_backward(d_rows: torch.Tensor, inv: torch.Tensor, out_dtype=None,
@@ -829,14 +839,12 @@ def moe_dispatch_backward(d_rows: torch.Tensor, inv: torch.Tensor, out_dtype=Non
     """The gradient of x from that of moe_dispatch's rows: each token's rows
     summed, [T][H] of out_dtype (d_rows' type)."""
     dev = _place(d_rows, inv, out)
-    if d_rows.dim() != 2:
-        raise ValueError("d_rows must be 2-D")
-    P, H = d_rows.shape
-    dtype, ld = _matrix(d_rows, H, "d_rows")
+    P, H, ld, dtype = _matrix(d_rows, "d_rows")
     T, k = _slots(inv)
-    dx, code, ld_dx = _result(out, d_rows, T, H, out_dtype or d_rows.dtype, stream)
+    dx, ld_dx, code = _result(out, d_rows, T, H, out_dtype or d_rows.dtype, stream)
     _enqueue((_lib or load()).moe_dispatch_backward, "moe_dispatch_backward", dev, stream,
-             _addr(d_rows), ld, P, dtype, _addr(inv), T, H, k, _addr(dx), ld_dx, code)
+             d_rows.data_ptr() or _UNREAD, ld, P, dtype, inv.data_ptr() or _UNREAD, T, H, k,
+             dx.data_ptr() or _UNREAD, ld_dx, code)
     return dx
 
 
@@ -847,20 +855,20 @@ def moe_combine(y: torch.Tensor, gates: torch.Tensor, inv: torch.Tensor,
     summed, plus its row of `shared` ([T][H] of y's type): [T][H] of out_dtype
     (y's type)."""
     dev = _place(y, gates, inv, shared, out)
-    if y.dim() != 2:
-        raise ValueError("y must be 2-D")
-    P, H = y.shape
-    dtype, ld = _matrix(y, H, "y")
+    P, H, ld, dtype = _matrix(y, "y")
     T, k = _slots(inv)
     _flat(gates, (T, k), torch.float32, "gates")
+    more = None
     ld_shared = 0
     if shared is not None:
-        code, ld_shared = _matrix(shared, H, "shared")
-        if code != dtype or shared.shape[0] != T:
-            raise ValueError(f"shared must have y's type and {T} rows")
-    res, code, ld_out = _result(out, y, T, H, out_dtype or y.dtype, stream)
-    _enqueue((_lib or load()).moe_combine, "moe_combine", dev, stream, _addr(y), ld, P, dtype,
-             _addr(gates), _addr(inv), _addr(shared), ld_shared, T, H, k, _addr(res), ld_out, code)
+        r, c, ld_shared, code = _matrix(shared, "shared")
+        if code != dtype or r != T or c != H:
+            raise ValueError(f"shared must have y's type and the shape {(T, H)}")
+        more = shared.data_ptr() or _UNREAD
+    res, ld_out, code = _result(out, y, T, H, out_dtype or y.dtype, stream)
+    _enqueue((_lib or load()).moe_combine, "moe_combine", dev, stream, y.data_ptr() or _UNREAD, ld,
+             P, dtype, gates.data_ptr() or _UNREAD, inv.data_ptr() or _UNREAD, more, ld_shared, T,
+             H, k, res.data_ptr() or _UNREAD, ld_out, code)
     return res
 
 
@@ -870,22 +878,20 @@ def moe_combine_backward(d_out: torch.Tensor, y: torch.Tensor, gates: torch.Tens
     fp32). Rows of d_y without a token are left as they were; that of `shared` is
     d_out."""
     dev = _place(d_out, y, gates, inv, out)
-    if y.dim() != 2:
-        raise ValueError("y must be 2-D")
-    P, H = y.shape
-    dtype, ld = _matrix(y, H, "y")
-    d_dtype, ld_d = _matrix(d_out, H, "d_out")
+    P, H, ld, dtype = _matrix(y, "y")
     T, k = _slots(inv)
-    if d_out.shape[0] != T:
-        raise ValueError(f"d_out must have {T} rows")
+    r, c, ld_d, d_dtype = _matrix(d_out, "d_out")
+    if r != T or c != H:
+        raise ValueError(f"d_out must have the shape {(T, H)}")
     _flat(gates, (T, k), torch.float32, "gates")
-    d_y, code, ld_dy = _result(out, y, P, H, y.dtype, stream)
+    d_y, ld_dy, code = _result(out, y, P, H, y.dtype, stream)
     if code != dtype:
         raise ValueError("out must have y's type")
     d_gates = _empty(gates, (T, k), torch.float32, stream)
     _enqueue((_lib or load()).moe_combine_backward, "moe_combine_backward", dev, stream,
-             _addr(d_out), ld_d, d_dtype, _addr(y), ld, P, dtype, _addr(gates), _addr(inv), T, H,
-             k, _addr(d_y), ld_dy, _addr(d_gates))
+             d_out.data_ptr() or _UNREAD, ld_d, d_dtype, y.data_ptr() or _UNREAD, ld, P, dtype,
+             gates.data_ptr() or _UNREAD, inv.data_ptr() or _UNREAD, T, H, k,
+             d_y.data_ptr() or _UNREAD, ld_dy, d_gates.data_ptr() or _UNREAD)
     return d_y, d_gates
 
 
@@ -900,10 +906,9 @@ def linear_w4_workspace_bytes(rows: int, experts: int, out_features: int, in_fea
 def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, out_dtype, out,
         workspace):
     """The checks and the call that both 4-bit products share; lead: () or (experts,)."""
-    if x.dim() != 2 or x.dtype != torch.bfloat16:
+    if x.dtype != torch.bfloat16:
         raise ValueError("x must be a 2-D bfloat16 tensor")
-    ld = _rows(x, "x")
-    M, K = x.shape
+    M, K, ld, _ = _matrix(x, "x")
     N = w.shape[-2]
     _flat(w, (*lead, N, K // 2), torch.uint8, "w")
     groups = w_scales.shape[-1]
@@ -911,16 +916,22 @@ def _w4(name, dev, stream, x, head, lead, w, w_scales, w_zeros, bias, swiglu, ou
     if scale is None or groups == 0 or K % groups:
         raise ValueError("w_scales must be float32 or bfloat16, its last dimension dividing x's")
     _flat(w_scales, (*lead, N, groups), w_scales.dtype, "w_scales")
-    _flat(w_zeros, (*lead, N, groups), torch.uint8, "w_zeros")
-    _flat(bias, (*lead, N), torch.float32, "bias")
-    res, code, ld_out = _result(out, x, M, N // 2 if swiglu else N, out_dtype, stream)
+    zeros = offset = None
+    if w_zeros is not None:
+        _flat(w_zeros, (*lead, N, groups), torch.uint8, "w_zeros")
+        zeros = w_zeros.data_ptr() or _UNREAD
+    if bias is not None:
+        _flat(bias, (*lead, N), torch.float32, "bias")
+        offset = bias.data_ptr() or _UNREAD
+    res, ld_out, code = _result(out, x, M, N // 2 if swiglu else N, out_dtype, stream)
     if workspace is None:
         need = linear_w4_workspace_bytes(M, lead[0] if lead else 1, N, K, code)
         if need:
             workspace = _empty(x, (need,), torch.uint8, stream)
-    _enqueue(getattr(_lib or load(), name), name, dev, stream, _addr(x), ld, *head, _addr(w),
-             _addr(w_scales), scale, _addr(w_zeros), _addr(bias), M, *lead, N, K, K // groups,
-             bool(swiglu), _addr(res), ld_out, code, _addr(workspace), _bytes(workspace))
+    _enqueue(getattr(_lib or load(), name), name, dev, stream, x.data_ptr() or _UNREAD, ld, *head,
+             w.data_ptr() or _UNREAD, w_scales.data_ptr() or _UNREAD, scale, zeros, offset, M,
+             *lead, N, K, K // groups, 1 if swiglu else 0, res.data_ptr() or _UNREAD, ld_out, code,
+             _addr(workspace), _bytes(workspace))
     return res
 
 
