@@ -329,6 +329,7 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
   };
   const auto unit = [&](int pass, int u) { return 128 * ((pass * W + w) * UW + u); };
   int buffer = 0;  // of the ring, of the strip that is multiplied next
+  int sums = 0;    // of the partial sums: in turn over all runs, as nothing else parts them
   locate(-1);
 #pragma unroll 1
   while (cur < end) {
@@ -460,7 +461,8 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
         }
       }
       if (at.pass + 1 == passes) {
-        float (*buf)[4][64] = part[(at.strip * per + at.half) & 1];
+        float (*buf)[4][64] = part[sums];
+        sums ^= 1;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           buf[w][v][lane] = acc[v];

@@ -332,6 +332,24 @@ def test_a_row_does_not_depend_on_the_batch_of_one_kernel():
             assert torch.equal(b, moe.moe_linear_w4(y, w, s, z, out_dtype=out))
 
 
+@pytest.mark.parametrize("N,K", [(35, 448), (80, 1024), (16, 2048), (48, 4096), (400, 64), (112, 8320)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_tiles_of_one_stream_are_those_of_calls_of_their_own(N, K, swiglu):
+    """An odd number of strips: workgroups go from one tile of 16 rows to the next."""
+    import block_fp8_routed_amd as moe
+    M = 1000 if N * K < 200_000 else 260
+    N += swiglu and N % 2
+    w, s, z, _ = weights((), N, K, 64 if K % 64 == 0 else 32, 19, zeros=N % 3 == 0)
+    x = activations(M, K, 20)
+    assert not takes_tiles(M, N, K, torch.float32)
+    whole = moe.moe_linear_w4(x, w, s, z, swiglu=swiglu, out_dtype=torch.float32)
+    for r in range(0, M, 16):
+        one = moe.moe_linear_w4(x[r:r + 16], w, s, z, swiglu=swiglu, out_dtype=torch.float32)
+        assert torch.equal(whole[r:r + 16], one), r
+    for _ in range(5):
+        assert torch.equal(whole, moe.moe_linear_w4(x, w, s, z, swiglu=swiglu, out_dtype=torch.float32))
+
+
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 512, 10, 256, 128), (16, 128, 8, 512, 192), (300, 8, 2, 256, 160),
                                         (2500, 8, 2, 512, 512)])
 @pytest.mark.parametrize("share", [False, True])
