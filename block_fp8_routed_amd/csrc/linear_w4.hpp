@@ -271,9 +271,12 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
   const uint32_t lds0 = lds_offset(mine);
   // This workgroup's share of all strips of all tiles, and the tile of its first one
   // (slot < 0) or the slot-th. Wavefront 0 looks it up for all.
-  int cur, end;  // (the host's limit: fewer than 2^23 strips of 16 rows)
+  int cur, end;
   const auto share = [&](int tiles) {
-    const uint64_t all = (uint64_t)(tiles * strips);
+    // (offsets that do not ascend could count rows twice: no more tiles than rows and
+    // experts allow; of the sizes that take the stream they are below 2^29 strips)
+    const int most = (int)p.M / TM + (int)(p.M < p.E ? p.M : p.E);
+    const uint64_t all = (uint64_t)(p.offsets && tiles > most ? most : tiles) * (uint64_t)strips;
     cur = __builtin_amdgcn_readfirstlane((int)(all * blockIdx.x / gridDim.x));
     end = __builtin_amdgcn_readfirstlane((int)(all * (blockIdx.x + 1) / gridDim.x));
   };

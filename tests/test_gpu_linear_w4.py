@@ -350,6 +350,19 @@ def test_tiles_of_one_stream_are_those_of_calls_of_their_own(N, K, swiglu):
         assert torch.equal(whole, moe.moe_linear_w4(x, w, s, z, swiglu=swiglu, out_dtype=torch.float32))
 
 
+def test_offsets_that_fall_count_no_row_twice_over():
+    """Offsets back and forth claim every row for every second expert: calls end, and
+    what lies outside the rows stays (which expert a row gets is not said)."""
+    import block_fp8_routed_amd as moe
+    E, M, N, K = 200, 90, 40, 128
+    w, s, z, _ = weights((E,), N, K, 128, 23)
+    x = activations(M, K, 24)
+    whole = torch.full((M + 8, N), 6.0, dtype=torch.float32, device="cuda")
+    offsets = torch.tensor([0, M] * (E // 2) + [0], dtype=torch.int32).cuda()
+    moe.moe_grouped_linear_w4(x, offsets, w, s, z, out=whole[:M])
+    assert bool((whole[M:] == 6).all()) and bool(torch.isfinite(whole).all())
+
+
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 512, 10, 256, 128), (16, 128, 8, 512, 192), (300, 8, 2, 256, 160),
                                         (2500, 8, 2, 512, 512)])
 @pytest.mark.parametrize("share", [False, True])
