@@ -399,15 +399,15 @@ __global__ __launch_bounds__(256) void combine_grad(
 }
 
 // ---------------------------------------------------------------- host side --
-// Tokens, hidden and the choice: 2^24 workgroups of 256 threads, and slots that
-// fit an int32 with the last chunk's end.
+// Tokens, hidden and the choice: fewer than 2^24 workgroups of 256 threads, and slots
+// that fit an int32 with the last chunk's end.
 static moe_status check_rows(int64_t tokens, int32_t H, int32_t k) {
   if (tokens < 0 || H <= 0 || k <= 0) return MOE_ERR_SHAPE;
   if (k > kMaxTopK || H > (1 << 20) || tokens >= ((int64_t)1 << 24) ||
       tokens * k > ((int64_t)1 << 27))
     return MOE_ERR_UNSUPPORTED;
-  // workgroups of one token and 256 columns at least
-  if (tokens * ((H + 255) / 256) >= ((int64_t)1 << 24)) return MOE_ERR_UNSUPPORTED;
+  // workgroups of one token and 256 columns at least (and one token's for the offsets)
+  if ((tokens + 1) * ((H + 255) / 256) >= ((int64_t)1 << 24)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

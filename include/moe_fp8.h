@@ -472,7 +472,7 @@ moe_status moe_swiglu_quantize_e4m3(const void* gate_up, int64_t ld, int64_t tok
  *   rows     (of the functions that read inv) the number of rows of d_rows, y and
  *            d_y. Rows of d_y without a slot stay as they were
  * Results overlap no input. top_k <= 16, experts <= 1024, hidden <= 2^20, tokens * top_k <=
- * 2^27, tokens * ceil(hidden / 256) < 2^24 (else MOE_ERR_UNSUPPORTED). The
+ * 2^27, (tokens + 1) * ceil(hidden / 256) < 2^24 (else MOE_ERR_UNSUPPORTED). The
  * workspace of moe_dispatch is moe_dispatch_workspace_bytes() (0: NULL is
  * allowed), 256-byte aligned; calls that overlap need one each. */
 size_t moe_dispatch_workspace_bytes(int64_t tokens, int32_t top_k, int32_t experts);

@@ -80,7 +80,8 @@ def test_row_distances_and_widths(f, lds):
     big = (1 << 20) + 1
     assert f(hidden=big, **{ld: big for ld in lds.split()}) == UNSUPPORTED
     wide = 1 << 20
-    assert f(hidden=wide, tokens=1 << 12, **{ld: wide for ld in lds.split()}) == UNSUPPORTED
+    for tokens in (1 << 12, (1 << 12) - 1):
+        assert f(hidden=wide, tokens=tokens, **{ld: wide for ld in lds.split()}) == UNSUPPORTED
 
 
 @pytest.mark.parametrize("f,kw,status", [
