@@ -502,15 +502,16 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  * second half u, and out[t][i] = silu(g_i) * u_i of out_features / 2 columns.
  * x is multiplied as it is, in fp32 sums that are rounded once to the output type. (zilda page, "Roadmap", and colizig page, "Status", name
  * 4-bit weights as a coming step; the format is a reading of this project.)
- *   x        [rows] rows of in_features bf16 values, finite, ld_x elements apart
- *            (a multiple of 8, at least in_features), 16-byte aligned
+ *   x        [rows] rows of in_features bf16 values, finite, below 2^120, ld_x
+ *            elements apart (a multiple of 8, at least in_features), 16-byte aligned.
+ *            A row with NaN or infinities spoils its own row of out only
  *   offsets  [experts + 1] int32, ascending, on the device; values are cut to
  *            [0, rows], and rows outside all experts' are left alone in out
  *   w        [experts][out_features][in_features / 2] bytes, 16-byte aligned: the
  *            code of an even column in a byte's low four bits, of the next one
  *            in its high four
  *   w_scales [experts][out_features][in_features / group], fp32 or bf16,
- *            magnitudes below 2^100
+ *            magnitudes below 2^90
  *   w_zeros  the same shape, a byte each, or NULL: every z is 8
  *   bias     [experts][out_features] fp32, or NULL for none
  *   out      [rows] rows of out_features values (half with swiglu) of out_dtype,

@@ -245,7 +245,7 @@ def test_a_row_of_nan_stays_in_its_row(M):
         assert torch.equal(got[rest], want[rest]) and bool(torch.isnan(got[5]).all())
 
 
-@pytest.mark.parametrize("scale", [2.0 ** 100, 2.0 ** -118])
+@pytest.mark.parametrize("scale", [2.0 ** 100, 2.0 ** -118, 2.0 ** 114])
 def test_ends_of_the_range(scale):
     """Large and small rows, their sums and the scales' products within fp32's range."""
     import block_fp8_routed_amd as moe
