@@ -12,7 +12,10 @@
 // All are bound by the bytes of the rows: a token's own row is read (or written)
 // once, its k others written (or read) once. So every kernel goes by token, with
 // the k rows' accesses of a thread's columns in flight together; sums are fp32
-// in the order of the slots, one rounding at the end.
+// in the order of the slots, one rounding at the end. Where a large copy moves 5.1
+// TB/s, reads alone 6: copies of a gradient of 369 MB take 63 us (5.9 TB/s), those of
+// a prompt of 369 MB 71 to 76 (5), combine of 403 MB 68 (5.9), combine_backward of 286
+// MB 59 (4.8).
 #include "device.hpp"
 #include "layer.hpp"
 #include "permute.hpp"
@@ -61,7 +64,8 @@ constexpr int kDispChunks = 64;    // placing workgroups at most
 // Workgroup t < T ranks the slots of token t against all others and copies its
 // row; workgroup T writes offsets. No workgroup needs another's result: a rank is
 // k comparisons a slot (wave-wide, counted by ballots), which for up to
-// kDispSmall slots costs less than a second launch. blockIdx.y: column chunks.
+// kDispSmall slots costs less than a second launch (512 tokens of 8 slots 11 us, 513
+// in three launches 12; one token 4.2). blockIdx.y: column chunks.
 template <class T, int N>
 __global__ __launch_bounds__(256) void dispatch_small(
     const T* __restrict__ x, int64_t ld_x, const int32_t* __restrict__ topk, int tokens, int H,
@@ -146,7 +150,8 @@ __global__ __launch_bounds__(256) void dispatch_small(
 }
 
 // ------------------------------------------------------------ three launches --
-// dispatch_count: workgroup b counts the slots of its chunk by expert.
+// dispatch_count: workgroup b counts the slots of its chunk by expert. (2.5 to 4.6 us,
+// dispatch_place 5 to 6.5.)
 __global__ __launch_bounds__(1024) void dispatch_count(const int32_t* __restrict__ topk, int64_t TK,
                                                        int64_t per, int E,
                                                        int32_t* __restrict__ counts) {

@@ -24,7 +24,8 @@ __device__ __forceinline__ uint32_t max_abs8(const uint4 v) {
 }
 
 // Rows of x as fp16 x 2^-e [M][Kp], zeros behind K, and e [M]. W wavefronts a row
-// (1: four rows a workgroup). Rows of up to 512 kHold W columns are read once.
+// (1: four rows a workgroup). Rows of up to 512 kHold W columns are read once. Bound by
+// its bytes: 32768 rows of 2048, 268 MB, 41 us (6.5 TB/s).
 template <int W>
 __global__ __launch_bounds__(256) void w4_halves(const uint16_t* __restrict__ x, int64_t ld_x,
                                                  int64_t M, int K, int Kp,
