@@ -500,8 +500,9 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  * expert e (offsets[e] <= t < offsets[e+1]) is multiplied with that expert's
  * matrix. With swiglu = 1 the first half of the features are gates g and the
  * second half u, and out[t][i] = silu(g_i) * u_i of out_features / 2 columns.
- * x is multiplied as it is, in fp32 sums that are rounded once to the output type. (zilda page, "Roadmap", and colizig page, "Status", name
- * 4-bit weights as a coming step; the format is a reading of this project.)
+ * x is multiplied as it is, in fp32 sums that are rounded once to the output type.
+ * (zilda page, "Roadmap", and colizig page, "Status", name 4-bit weights as a coming
+ * step; the format is a reading of this project.)
  *   x        [rows] rows of in_features bf16 values, finite, below 2^120, ld_x
  *            elements apart (a multiple of 8, at least in_features), 16-byte aligned.
  *            A row with NaN or infinities spoils its own row of out only
