@@ -317,6 +317,33 @@ def test_offsets_are_cut_to_the_rows(M, N, K):
     check(out[:4], ref[:4], err[:4])
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K", [512, 4160])
+def test_rows_of_no_expert_take_no_part_in_tiles(out, K):
+    """Rows before the first and behind the last expert's, and what the workspace held."""
+    import block_fp8_routed_amd as moe
+    E, M, N, first, last = 3, 2000, 2048, 37, 911
+    w, s, z, b = weights((E,), N, K, 32, 29, bias=True)
+    x = activations(M, K, 30)
+    assert takes_tiles(M, N, K, out, E)
+    offsets = torch.tensor([first, 300, 300, last], dtype=torch.int32).cuda()
+    code = moe.MOE_BF16 if out == torch.bfloat16 else moe.MOE_F32
+    need = moe.linear_w4_workspace_bytes(M, E, N, K, code)
+    got = []
+    for fill in (0, 255):
+        work = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        y = torch.full((M, N), 5.0, dtype=out, device="cuda")
+        rest = x.clone()
+        rest[:first] = float("nan") if fill else 1
+        rest[last:] = float("nan") if fill else 1
+        moe.moe_grouped_linear_w4(rest, offsets, w, s, z, bias=b, out_dtype=out, out=y, workspace=work)
+        got.append(y)
+    assert torch.equal(*got) and bool((got[0][:first] == 5).all() and (got[0][last:] == 5).all())
+    for lo, hi, e in ((first, 300, 0), (300, last, 2)):
+        ref, err = reference(x[lo:hi], w[e], s[e], z[e], b[e], False, half=out == torch.bfloat16)
+        check(got[0][lo:hi], ref, err)
+
+
 def test_a_row_does_not_depend_on_the_batch_of_one_kernel():
     """Rows of a batch of one size keep their bits whatever the other rows hold."""
     import block_fp8_routed_amd as moe
