@@ -501,13 +501,15 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
 // (and off by at most 2^-40 of it below). w4_halves writes such rows to the
 // workspace, with columns in the order in which codes leave a dword.
 //   W: a masked code is the fp16 subnormal q 2^-24 (16 q 2^-24 for the upper four
-// bits of a byte), so one multiply-add with S = s 2^24 and -z s makes it (q - z) s:
-// nine instructions for eight weights. The weights' row has a power of two that
-// brings its largest s into [2^-10, 2^-9), S below 2^15. S, z s and the result round
-// once each, to half a step of 11 bits or 2^-25: at most (2^-10 |q - z| + 2^-11 z) s
-// and 2^-14 of the row's largest scale, 3e-4 of the result in norm beside the
-// 1.7e-3 of its rounding to bf16. (The exact form takes a multiply-add on each sum
-// and group besides.)
+// bits of a byte), so one multiply-add with 2^15 (2^11) and -z 2^-9 makes it
+// (q - z) 2^-9, exact, and one multiplication with S the weight: 13 instructions for
+// eight. S is s times the power of two of the weights' row that brings its largest
+// into [2^14, 2^15). S and the product are rounded to fp16's 11 bits, which moves a
+// weight by at most 2^-10 of itself (S of a bf16 scale is exact: by 2^-11), and by
+// 2^-29 of the row's largest scale where it is below fp16's normal numbers.
+// (z s is never rounded apart from q s: what that leaves is common to a group's
+// columns, and adds up over rows that have a mean. The exact form takes a multiply-add
+// on each sum and group besides.)
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -530,16 +532,22 @@ __device__ __forceinline__ void w4_tile_of(int b, int tiles_m, int tiles_n, int&
   tn = band * kBand + in - tm * width;
 }
 
-// Eight codes of a dword as (q - z) s in fp16, in the column order of half_order:
-// S = s 2^24, S16 = S / 16, zs = -z s.
-__device__ __forceinline__ f16x8_t codes_f16(uint32_t d, f16x2_t S, f16x2_t S16, f16x2_t zs) {
+// Eight codes of a dword as (q - z) 2^-9 in fp16, exact, in the column order of
+// half_order; zero: -z 2^-9.
+__device__ __forceinline__ f16x2_t zero_f16(float z) {
+  const _Float16 v = (_Float16)(-0x1p-9f * z);
+  return f16x2_t{v, v};
+}
+__device__ __forceinline__ f16x8_t codes_f16(uint32_t d, f16x2_t zero) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const f16x2_t one = {(_Float16)0x1p15f, (_Float16)0x1p15f};
+  const f16x2_t one16 = {(_Float16)0x1p11f, (_Float16)0x1p11f};
   const uint32_t d8 = d >> 8;
   const auto low = [&](uint32_t v) {
-    return __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, v & 0x000f000fu), S, zs);
+    return __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, v & 0x000f000fu), one, zero);
   };
   const auto high = [&](uint32_t v) {
-    return __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, v & 0x00f000f0u), S16, zs);
+    return __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, v & 0x00f000f0u), one16, zero);
   };
   const u32x4 v = {__builtin_bit_cast(uint32_t, low(d)), __builtin_bit_cast(uint32_t, high(d)),
                    __builtin_bit_cast(uint32_t, low(d8)), __builtin_bit_cast(uint32_t, high(d8))};
@@ -708,7 +716,7 @@ __global__ __launch_bounds__(256, 2) void w4_tile(W4Args p, const uint16_t* __re
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const float m = tops[32 * j + l32];
-    en[j] = m > 0.f ? __builtin_amdgcn_frexp_expf(m) + 9 : 0;
+    en[j] = m > 0.f ? __builtin_amdgcn_frexp_expf(m) - 6 : 0;  // the weights' power of two
   }
   f32x16 acc[2][FM];
 #pragma unroll
@@ -726,19 +734,17 @@ __global__ __launch_bounds__(256, 2) void w4_tile(W4Args p, const uint16_t* __re
       ld.issue(kb + 1);
       ld.fetch(kb + 1, next);
     }
-    f16x2_t S[2][NS], S16[2][NS], zs[2][NS];
+    f16x8_t S[2][NS];
+    f16x2_t zero[2][NS];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
         float sv, zv;
         ld.scale_of(kb, j, G == 128 ? 0 : G == 64 ? h : 2 * h + i, sv, zv);
-        const _Float16 v = (_Float16)__builtin_ldexpf(sv, 24 - en[j]);
-        const _Float16 z = (_Float16)(-0x1p-24f * (float)v * zv);
-        const _Float16 v16 = v * (_Float16)0.0625f;
-        S[j][i] = f16x2_t{v, v};
-        S16[j][i] = f16x2_t{v16, v16};
-        zs[j][i] = f16x2_t{z, z};
+        const _Float16 v = (_Float16)__builtin_ldexpf(sv, 9 - en[j]);
+        S[j][i] = f16x8_t{v, v, v, v, v, v, v, v};
+        zero[j][i] = zero_f16(zv);
       }
 #pragma unroll
     for (int j = 0; j < 2; ++j) L::pieces(c[j]);
@@ -750,7 +756,7 @@ __global__ __launch_bounds__(256, 2) void w4_tile(W4Args p, const uint16_t* __re
         const uint4 q = c[j][i / 4];
         const uint32_t d[4] = {q.x, q.y, q.z, q.w};
         constexpr int kEach = 8 / NS;
-        w[j] = codes_f16(d[i % 4], S[j][i / kEach], S16[j][i / kEach], zs[j][i / kEach]);
+        w[j] = codes_f16(d[i % 4], zero[j][i / kEach]) * S[j][i / kEach];
       }
 #pragma unroll
       for (int m = 0; m < FM; ++m) {
@@ -860,8 +866,6 @@ __global__ __launch_bounds__(256, 2) void w4_tile_exact(W4Args p, const uint16_t
     for (int m = 0; m < FM; ++m)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[j][m][v] = 0.f;
-  const f16x2_t one = {(_Float16)0x1p15f, (_Float16)0x1p15f};
-  const f16x2_t one16 = {(_Float16)0x1p11f, (_Float16)0x1p11f};
 #pragma unroll 1
   for (int kb = 0; kb < ld.stages; ++kb) {
     w4_wait<0>();
@@ -893,10 +897,9 @@ __global__ __launch_bounds__(256, 2) void w4_tile_exact(W4Args p, const uint16_t
       for (int j = 0; j < 2; ++j) {
         float z;
         ld.scale_of(kb, j, g, s[j], z);
-        const _Float16 zv = (_Float16)(-0x1p-9f * z);
-        const f16x2_t zs = {zv, zv};
+        const f16x2_t zero = zero_f16(z);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) w[j][i] = codes_f16(d[j][g * NI + i], one, one16, zs);
+        for (int i = 0; i < NI; ++i) w[j][i] = codes_f16(d[j][g * NI + i], zero);
       }
 #pragma unroll
       for (int m = 0; m < FM; ++m) {

@@ -522,9 +522,9 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  * in_features; out_features is free, but even with swiglu. A row's result does not
  * depend on the other rows' values; which kernel a call takes goes by its sizes
  * and output type. Larger batches with bf16 output multiply with weights rounded to
- * fp16, an error of at most (2^-10 |q - z| + 2^-11 z) s and 2^-14 of the row's largest
- * scale in each weight, 3e-4 of the result in norm beside the 1.7e-3 of its rounding
- * to bf16; all else is exact up to fp32's own rounding. experts <= 1024;
+ * fp16, each off by at most 2^-10 of itself (2^-11 with bf16 scales) and 2^-29 of the
+ * row's largest scale, so that one with q = z is 0; all else is exact up to fp32's own
+ * rounding. experts <= 1024;
  * in_features, out_features, rows <= 2^20; (rows/32 + experts) * ceil(out_features/128)
  * < 2^24 (else MOE_ERR_UNSUPPORTED). rows == 0 enqueues nothing. The workspace is
  * moe_linear_w4_workspace_bytes() of the same sizes, experts = 1 for moe_linear_w4 (0
