@@ -955,19 +955,36 @@ inline int64_t row_tiles(const W4Args& p, int TM) {
   return p.offsets ? p.M / TM + (p.M < p.E ? p.M : p.E) : (p.M + TM - 1) / TM;
 }
 
+// Columns that the stream multiplies for each strip: those of all its wavefronts' units
+// (launch_w4), whether K fills them or not, once more for each pass.
+constexpr int kW4Pass = 4096;
+inline int w4_span(int K) {
+  if (K <= 2048) return K <= 768 ? 768 : K <= 1024 ? 1024 : 2048;
+  return (K + kW4Pass - 1) / kW4Pass * kW4Pass;
+}
+
 // Which kernel a product runs on: the one that is reckoned to take less time (us on one
 // MI355X, weights in no cache). The weights of the experts that can have a row, read
 // once, take W = E N K / 10^7.
-//   stream  8 + 5.4e-9 M N K + 0.75 W   (4096 x 4096, 128 / 512 / 1024 rows: 21 / 54 / 99; 128
-//           experts of 2048 x 2048, 32 / 64 / 96 rows each: 143 / 233 / 331)
-//   tiles   10 + 2.5e-9 (M + 32 E) N K + W, at least 6 + 1.45 a stage + W; fp32 output 2.9e-9
-//           (M + 48 E): E short tiles (54 / 57 / 63, fp32 52 / 56 / 68; 146 / 190 / 241, fp32 169 / 238 / 284)
+//   stream  8 + 5.4e-9 (M + 10 (E - 1)) N span + 0.75 W: E short tiles; the second term
+//           twice where x is read again for every pass (4096 x 4096, 128 / 512 / 1024 rows: 21 / 54 / 99; 128 experts of
+//           2048 x 2048, 32 / 64 / 96 rows each: 143 / 233 / 331; 4096 rows, 4096 x 32:
+//           92; 1024 rows, 4096 x 128: 23; 256 rows, 4096 x 4096 / 4128: 27 / 103; 103 rows of 222
+//           experts of 8026 x 192: 62)
+//   tiles   12.5 + 2.5e-9 (M + 32 E) N K + W, at least 8 + 1.45 a stage + W; fp32 output
+//           2.9e-9 (M + 48 E): E short tiles (the same sizes: 54 / 57 / 63, fp32 52 / 56 /
+//           68; 146 / 190 / 241, fp32 169 / 238 / 284; 20, fp32 34; 14, 17; 44 / 69, 43 / 58;
+//           fp32 34)
+// (Of 848 products of 16 to 16384 rows, 64 to 8192 features and 32 to 8192 columns it
+// takes one that is over 1.1 times as slow as the other in 28, 1.45 times at most; most of
+// those are short, where the host's 2.5 us for a second launch count.)
 enum W4Form { kW4Stream, kW4Tiles };
 inline W4Form w4_form(int64_t M, int E, int N, int K, bool bf16) {
   const double experts = (double)(M < E ? M : E), NK = (double)N * K, W = experts * NK * 1e-7;
-  const double stream = 8.0 + 5.4e-9 * M * NK + 0.75 * W;
-  const double busy = 10.0 + (bf16 ? 2.5e-9 * (M + 32 * experts) : 2.9e-9 * (M + 48 * experts)) * NK;
-  const double stages = 6.0 + 1.45 * ((K + kW4Stage - 1) / kW4Stage);
+  const double stream =
+      8.0 + (K > kW4Pass ? 10.8e-9 : 5.4e-9) * (M + 10 * (experts - 1)) * N * w4_span(K) + 0.75 * W;
+  const double busy = 12.5 + (bf16 ? 2.5e-9 * (M + 32 * experts) : 2.9e-9 * (M + 48 * experts)) * NK;
+  const double stages = 8.0 + 1.45 * ((K + kW4Stage - 1) / kW4Stage);
   return stream <= W + (busy > stages ? busy : stages) ? kW4Stream : kW4Tiles;
 }
 
@@ -1031,7 +1048,7 @@ void launch_w4(const W4Args& p, void* workspace, hipStream_t s) {
     if (p.K <= 768) return launch_stream<G, SB, Z, 2, 3, false>(p, s);
     if (p.K <= 1024) return launch_stream<G, SB, Z, 2, 4, false>(p, s);
     if (p.K <= 2048) return launch_stream<G, SB, Z, 4, 4, false>(p, s);
-    if (p.K <= 4096) return launch_stream<G, SB, Z, 8, 4, false>(p, s);
+    if (p.K <= kW4Pass) return launch_stream<G, SB, Z, 8, 4, false>(p, s);
     return launch_stream<G, SB, Z, 8, 4, true>(p, s);
   }
   const int Kp = w4_padded(p.K);
