@@ -497,8 +497,8 @@ __global__ __launch_bounds__(64 * W, 2) void w4_stream(W4Args p) {
 // zero point are in the weight itself and the matrix instructions run one chain of
 // sums over all of K.
 //   x: bf16 has 8 significant bits and fp16 11, so a row times a power of two that
-// brings its largest magnitude below 2^15 is exact down to 2^-29 of that magnitude
-// (and off by at most 2^-40 of it below). w4_halves writes such rows to the
+// brings its largest magnitude into [2^14, 2^15) is exact down to 2^-29 of that
+// magnitude (and off by at most 2^-25, 2^-39 of it, below). w4_halves writes such rows to the
 // workspace, with columns in the order in which codes leave a dword.
 //   W: a masked code is the fp16 subnormal q 2^-24 (16 q 2^-24 for the upper four
 // bits of a byte), so one multiply-add with 2^15 (2^11) and -z 2^-9 makes it
@@ -967,14 +967,14 @@ inline int w4_span(int K) {
 // MI355X, weights in no cache). The weights of the experts that can have a row, read
 // once, take W = E N K / 10^7.
 //   stream  8 + 5.4e-9 (M + 10 (E - 1)) N span + 0.75 W: E short tiles; the second term
-//           twice where x is read again for every pass (4096 x 4096, 128 / 512 / 1024 rows: 21 / 54 / 99; 128 experts of
-//           2048 x 2048, 32 / 64 / 96 rows each: 143 / 233 / 331; 4096 rows, 4096 x 32:
-//           92; 1024 rows, 4096 x 128: 23; 256 rows, 4096 x 4096 / 4128: 27 / 103; 103 rows of 222
-//           experts of 8026 x 192: 62)
+//           twice where x is read again for every pass. 4096 x 4096, 128 / 512 / 1024 rows:
+//           21 / 54 / 99; 128 experts of 2048 x 2048, 32 / 64 / 96 rows each: 143 / 233 /
+//           331; 4096 rows, 4096 x 32: 92; 1024 rows, 4096 x 128: 23; 256 rows, 4096 x 4096
+//           / 4128: 27 / 103; 103 rows of 222 experts of 8026 x 192: 62
 //   tiles   12.5 + 2.5e-9 (M + 32 E) N K + W, at least 8 + 1.45 a stage + W; fp32 output
-//           2.9e-9 (M + 48 E): E short tiles (the same sizes: 54 / 57 / 63, fp32 52 / 56 /
-//           68; 146 / 190 / 241, fp32 169 / 238 / 284; 20, fp32 34; 14, 17; 44 / 69, 43 / 58;
-//           fp32 34)
+//           2.9e-9 (M + 48 E): E short tiles. The same sizes: 54 / 57 / 63, fp32 52 / 56 /
+//           68; 146 / 190 / 241, fp32 169 / 238 / 284; 20, fp32 34; 14, 17; 44 / 69, 43 /
+//           58; fp32 34
 // (Of 848 products of 16 to 16384 rows, 64 to 8192 features and 32 to 8192 columns it
 // takes one that is over 1.1 times as slow as the other in 28, 1.45 times at most; most of
 // those are short, where the host's 2.5 us for a second launch count.)

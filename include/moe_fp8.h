@@ -523,8 +523,10 @@ moe_status moe_combine_backward(const void* d_out, int64_t ld_d, moe_dtype d_dty
  * depend on the other rows' values; which kernel a call takes goes by its sizes
  * and output type. Larger batches with bf16 output multiply with weights rounded to
  * fp16, each off by at most 2^-10 of itself (2^-11 with bf16 scales) and 2^-29 of the
- * row's largest scale, so that one with q = z is 0; all else is exact up to fp32's own
- * rounding. experts <= 1024;
+ * row's largest scale, so that one with q = z is 0. Larger batches of either output
+ * type hold a row of x to 2^-39 of its largest magnitude. All else is exact up to fp32's
+ * own rounding, in small batches of sum x q and z sum x apart. The sums of |x W| have to
+ * be within fp32's range. experts <= 1024;
  * in_features, out_features, rows <= 2^20; (rows/32 + experts) * ceil(out_features/128)
  * < 2^24 (else MOE_ERR_UNSUPPORTED). rows == 0 enqueues nothing. The workspace is
  * moe_linear_w4_workspace_bytes() of the same sizes, experts = 1 for moe_linear_w4 (0

@@ -6,7 +6,9 @@ to [2^14, 2^15), is rounded once to fp16's 11 bits, and so is the product S (q -
 2^-11 of the weight each time, 2^-10 (1 + 2^-12) of it together. Below fp16's normal
 numbers a rounding is off by up to 2^-25 instead; beside 2^14 2^-9, the smallest that the
 largest scale is there, 2^-30 of that scale for the product, 2^-39 |q - z| of it for S.
-fp32 sums as in test_gpu_linear_w4.py.
+fp32 sums as in test_gpu_linear_w4.py. A row of x is fp16 times the power of two that
+brings its largest magnitude to 2^14 at least: half a step of fp16's smallest numbers,
+2^-25, is up to 2^-39 of it.
 The bound in norm. A rounding to 11 bits is off by 2^-11 / sqrt(3) of the value at most in
 the mean square. Products round each for itself, S once a group: with codes drawn evenly
 about the zero point the terms of a sum are as good as independent between columns and
@@ -35,7 +37,7 @@ def bound(x, w, s, z):
     v, mag, _ = values(w, s, z)
     a, top = np.abs(x), s.double().abs().amax(dim=1).cpu().numpy()
     err = ((64 + x.shape[1] / 32) * 2.0 ** -24 * (a @ mag.T)
-           + 2.0 ** -40 * a.max(axis=1)[:, None] * np.abs(v).sum(axis=1)
+           + 2.0 ** -39 * a.max(axis=1)[:, None] * np.abs(v).sum(axis=1)
            + 2.0 ** -10 * (1 + 2.0 ** -12) * (a @ np.abs(v).T)
            + (2.0 ** -30 + 255 * 2.0 ** -39) * a.sum(axis=1)[:, None] * top)
     return x @ v.T, err, np.sqrt((x * x) @ (v * v).T)
