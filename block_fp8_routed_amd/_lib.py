@@ -758,7 +758,9 @@ def moe_swiglu_quantize_e4m3(gate_up: torch.Tensor, stream=None):
 
 # ---- rows to their experts and back, and products with 4-bit weights ----
 # (At decode sizes a call's checks take longer than its kernel: tensors are asked
-# for each property once.)
+# for each property once. Like the rest of this package they record no autograd graph:
+# results never require gradients, whatever the arguments do. In a graph they go into a
+# torch.autograd.Function whose backward calls the *_backward functions.)
 def _matrix(t: torch.Tensor, what: str):
     """(rows, columns, distance of rows, moe_dtype) of a 2-D fp32 or bf16 tensor with
     contiguous rows."""
@@ -807,7 +809,8 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, experts: int,
     """The rows of x [T][H] (fp32 or bf16; rows may lie apart) sorted by their
     experts topk_idx [T][k] int32: (rows [T*k][H], offsets [experts+1], pair [T*k],
     inv [T][k], all int32). Choices outside [0, experts) get no row (inv -1); rows
-    behind offsets[experts] are left as they were (pair -1)."""
+    behind offsets[experts] are left as they were (pair -1). No autograd graph is
+    recorded: the gradient of x is moe_dispatch_backward's."""
     dev = _place(x, topk_idx, out, workspace)
     T, H, ld, dtype = _matrix(x, "x")
     if topk_idx.dim() != 2:
@@ -853,7 +856,8 @@ def moe_combine(y: torch.Tensor, gates: torch.Tensor, inv: torch.Tensor,
                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Each token's rows of y (moe_dispatch's order) times its gates [T][k] fp32,
     summed, plus its row of `shared` ([T][H] of y's type): [T][H] of out_dtype
-    (y's type)."""
+    (y's type). No autograd graph is recorded: the gradients of y and gates are
+    moe_combine_backward's."""
     dev = _place(y, gates, inv, shared, out)
     P, H, ld, dtype = _matrix(y, "y")
     T, k = _slots(inv)
@@ -944,7 +948,7 @@ def moe_linear_w4(x: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
     (q - z) s: w [N][K/2] uint8 (the even column in the low four bits), w_scales
     [N][K/group] fp32 or bf16 (group 32, 64 or 128), w_zeros the same shape uint8
     (8 without), plus an optional fp32 bias [N]. swiglu: silu(first half of the
-    features) times the second half, [T][N/2]."""
+    features) times the second half, [T][N/2]. There is no gradient."""
     dev = _place(x, w, w_scales, w_zeros, bias, out, workspace)
     if w.dim() != 2:
         raise ValueError("w must be 2-D")
@@ -959,7 +963,8 @@ def moe_grouped_linear_w4(x: torch.Tensor, offsets: torch.Tensor, w: torch.Tenso
                           workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """moe_linear_w4 by expert: rows offsets[e] .. offsets[e+1]-1 of x (moe_dispatch's
     order) times expert e's weight; w [E][N][K/2], w_scales and w_zeros
-    [E][N][K/group], bias [E][N]. Rows outside all experts' are left as they were."""
+    [E][N][K/group], bias [E][N]. Rows outside all experts' are left as they were.
+    There is no gradient."""
     dev = _place(x, offsets, w, w_scales, w_zeros, bias, out, workspace)
     if w.dim() != 3:
         raise ValueError("w must be 3-D")
