@@ -232,8 +232,10 @@ __device__ __forceinline__ uint32_t lds_offset(T* p) {
 // and the strip of their ups follow each other; the thread that adds a gate's
 // partial sums keeps it for its up's.
 //   Measured: one layer's banks of a decode batch, 197 MB in two calls, 48 to 52 us (4
-// TB/s); 321 MB of one bank 64 us (5.0 TB/s). 128 rows of 4096 x 4096: 18 us, bound by
-// the conversions and products (22 with x read again from the L2 for each strip).
+// TB/s); 321 MB of one bank 64 us (5.0 TB/s). 128 rows of 4096 x 4096: 18 us, of
+// which vector instructions (exchange, conversions, scales) fill 8 and matrix instructions
+// 2; two wavefronts a SIMD wait for the rest (22 with x read again from the L2 for each
+// strip).
 template <int G, bool Z, int W, int UW, int KB>
 struct StreamRing {
   static constexpr int kGroups = UW * 128 / G;          // a wavefront's groups in a row
@@ -669,8 +671,8 @@ struct TileLoads {
 };
 
 // bf16 output. What bounds it is the matrix unit and the vector unit that makes its
-// weights, side by side: 4096 x 8192 x 4096 takes 245 us (1.12 PFLOP/s), of whose
-// cycles matrix instructions fill 55 %, vector instructions 37 % and LDS 16 %.
+// weights, side by side: 4096 x 8192 x 4096 takes 252 us (1.09 PFLOP/s), of whose
+// cycles matrix instructions fill 54 %, vector instructions 41 % and LDS 16 %.
 // Lane l holds columns 64 h .. 64 h + 63 of row l % 32 of either operand,
 // h = l / 32; instruction i takes eight of them.
 template <int G, bool SB, bool Z, int FM>
@@ -841,8 +843,8 @@ __global__ __launch_bounds__(256, 2) void w4_tile(W4Args p, const uint16_t* __re
 // one group follow each other in one accumulator. The codes are the B operand: a lane
 // holds one output feature, whose scale it reads itself, and 32 lanes store a line.
 //   The multiply-adds on each sum and group bound it: one group of 32 columns is two
-// products of 32 cycles and 16 multiply-adds of 4. 4096 x 8192 x 4096: 306 us in groups
-// of 128 (0.90 PFLOP/s), 493 in groups of 32.
+// products of 32 cycles and 16 multiply-adds of 4. 4096 x 8192 x 4096, a call: 310 us in
+// groups of 128 (0.89 PFLOP/s), 405 in groups of 32; 338 and 494 with zero points.
 template <int G, bool SB, bool Z, int FM>
 __global__ __launch_bounds__(256, 2) void w4_tile_exact(W4Args p, const uint16_t* __restrict__ xh,
                                                         const int32_t* __restrict__ xe, int Kp,
