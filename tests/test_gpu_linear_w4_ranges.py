@@ -71,3 +71,37 @@ def test_scales_at_the_ends_of_their_range(M, N, K, G, scale, row):
         else:
             ref, err = reference(x, w, s, z, None, False, False)
         check(moe.moe_linear_w4(x, w, s, z, out_dtype=out), ref, err + tiny, str(out))
+
+
+@pytest.mark.parametrize("M,N,K,G", [(4096, 4096, 32, 32), (4100, 1290, 64, 64), (4100, 1290, 64, 32),
+                                     (4097, 1300, 128, 128), (3000, 2050, 96, 32), (4100, 1284, 192, 64),
+                                     (1030, 1282, 4128, 32), (260, 4100, 4160, 64)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_few_columns_and_a_few_past_a_pass_on_tiles(M, N, K, G, swiglu):
+    import block_fp8_routed_amd as moe
+    for i, out in enumerate(TYPES.values()):
+        assert takes_tiles(M, N, K, out)
+        w, s, z, b = weights((), N, K, G, M + i, "bf16" if i else "f32", i == 0, True)
+        s = s * (0.03 if swiglu else 1)
+        x = activations(M, K, M)
+        got = moe.moe_linear_w4(x, w, s, z, bias=b, swiglu=swiglu, out_dtype=out)
+        if out == torch.bfloat16 and not swiglu:
+            y, err, _ = bound(x, w, s, z)
+            b = b.double().cpu().numpy()
+            ref, err = y + b, err + 2.0 ** -24 * (np.abs(y) + np.abs(b))
+        else:
+            ref, err = reference(x, w, s, z, b, swiglu, out == torch.bfloat16)
+        check(got, ref, err, str(out))
+
+
+@pytest.mark.parametrize("M,E,N,K,G", [(103, 222, 8026, 192, 64), (565, 38, 704, 4224, 128)])
+def test_short_tiles_of_experts(M, E, N, K, G):
+    import block_fp8_routed_amd as moe
+    assert takes_tiles(M, N, K, torch.float32, E)
+    r = np.random.default_rng(M)
+    offsets = np.searchsorted(np.sort(r.integers(0, E, M)), np.arange(E + 1)).astype(np.int32)
+    w, s, z, b = weights((E,), N, K, G, 5, bias=True)
+    x = activations(M, K, 6)
+    got = moe.moe_grouped_linear_w4(x, torch.from_numpy(offsets).cuda(), w, s, z, bias=b,
+                                    out_dtype=torch.float32)
+    check(got, *grouped_reference(x, offsets, w, s, z, b, False, False))
